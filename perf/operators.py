@@ -586,6 +586,7 @@ def _own_state(s):
     case, op = s["case"], s["case"]["op"]
     s["rq"] = rq
     if op == "tree":
+        s["R"] = s["R"].contiguous()               # the library takes R row by row
         cfg = rq.rq_config(1, _P, 1, case["H"], case["d"], case["g"], case["B"], s["nt"] * 64, rq.RQ_MODE_SHARED,
                            case["Hq"])
         if case["paged"]:
@@ -605,6 +606,8 @@ def _own_state(s):
                            case["tiles"] * 64, rq.RQ_MODE_HADAMARD if case["d"] == 128 else rq.RQ_MODE_SHARED, 0)
         R = None if case["d"] == 128 else torch.eye(case["d"], device=s["pool"].device)
         s["R"] = R
+        if op == "copy":                           # lists start on a 16-byte boundary
+            s.update(src=s["src"].clone(), dst=s["dst"].clone())
         h = rq.rq_cache_create_paged(cfg, case["pages"], s["pool"], s["pool"].numel(), s["table"],
                                      s["table"].shape[1], R)
         size = rq.rq_pages_workspace_bytes(cfg, case["pages"])
