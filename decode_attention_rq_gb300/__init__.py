@@ -19,6 +19,10 @@ __all__ = [
     "rq_decode_attention_bf16", "rq_status_string", "EXPORTED_SYMBOLS",
     "rq_decode_attention_noalloc", "RQ_NOALLOC_WORKSPACE_BYTES", "rq_decode_attention_append",
     "rq_cache_paged_bytes", "rq_cache_create_paged",
+    "rq_tree_workspace_bytes", "rq_tree_attention", "RQ_MAX_TREE_NODES",
+    "rq_pages_workspace_bytes", "rq_pages_copy", "rq_pages_fork", "rq_pages_reserve", "rq_pages_free",
+    "rq_pages_compact",
+    "rq_rope", "rq_rope_config", "RQ_ROPE_PLAIN", "RQ_ROPE_LINEAR", "RQ_ROPE_BASE", "RQ_ROPE_PARTS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librq.so")
@@ -36,10 +40,16 @@ EXPORTED_SYMBOLS = (
     "rq_decode_workspace_bytes", "rq_decode_attention", "rq_bf16_workspace_bytes",
     "rq_decode_attention_bf16", "rq_status_string", "rq_decode_attention_noalloc",
     "rq_decode_attention_append", "rq_cache_paged_bytes", "rq_cache_create_paged",
+    "rq_tree_workspace_bytes", "rq_tree_attention", "rq_pages_workspace_bytes", "rq_pages_copy",
+    "rq_pages_fork", "rq_pages_reserve", "rq_pages_free", "rq_pages_compact", "rq_rope",
 )
 
 # size of the workspace built into the library for rq_decode_attention_noalloc (rq.h)
 RQ_NOALLOC_WORKSPACE_BYTES = 2 * 1024 * 1024
+# drafted tokens per row that one rq_tree_attention call may cover (rq.h)
+RQ_MAX_TREE_NODES = 256
+# frequency scalings of rq_rope (rq.h)
+RQ_ROPE_PLAIN, RQ_ROPE_LINEAR, RQ_ROPE_BASE, RQ_ROPE_PARTS = 0, 1, 2, 3
 
 
 class RqError(RuntimeError):
@@ -53,6 +63,19 @@ class rq_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "num_layers", "loops_per_group", "num_groups", "num_heads", "head_dim", "group_size",
         "max_batch", "max_seq_len", "mode", "num_query_heads")]
+
+
+class rq_rope_config(ctypes.Structure):
+    """rq.h's rq_rope_config: how rq_rope turns a head."""
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "head_dim", "rotary_dim", "interleaved", "inverse", "scaling", "original_len")] + [
+        (n, ctypes.c_double) for n in ("theta", "factor", "low_turns", "high_turns", "magnitude")]
+
+
+class _rope_tensor(ctypes.Structure):
+    """rq.h's rq_rope_tensor."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int32)] + [
+        (n, ctypes.c_int64) for n in ("in_row", "in_head", "in_token", "out_row", "out_head", "out_token")]
 
 
 if not os.path.exists(LIB_PATH):
@@ -85,6 +108,25 @@ lib.rq_bf16_workspace_bytes.argtypes = [_i32, _i32, _i32]
 lib.rq_bf16_workspace_bytes.restype = _sz
 lib.rq_decode_attention_bf16.argtypes = [_p, _p, _p, _p, _p, _p, _i32, _i32, _i32, _i32, _f, _p, _p, _sz, _p]
 lib.rq_decode_attention_bf16.restype = ctypes.c_int
+lib.rq_tree_workspace_bytes.argtypes = [_cfgp, _i32, _i32]
+lib.rq_tree_workspace_bytes.restype = _sz
+lib.rq_tree_attention.argtypes = [_p, _i32, _i32, _i32, _i32, _i32, _p, _p, _p, _p, _p, _p, _f, _p, _p, _sz, _p]
+lib.rq_tree_attention.restype = ctypes.c_int
+lib.rq_pages_workspace_bytes.argtypes = [_cfgp, _i32]
+lib.rq_pages_workspace_bytes.restype = _sz
+lib.rq_pages_copy.argtypes = [_p, _i32, _p, _p, _p, _p]
+lib.rq_pages_copy.restype = ctypes.c_int
+lib.rq_pages_fork.argtypes = [_p, _i32, _p, _p, _p, _p, _p]
+lib.rq_pages_fork.restype = ctypes.c_int
+lib.rq_pages_reserve.argtypes = [_p, _i32, _p, _i32, _p, _p, _p, _sz, _p]
+lib.rq_pages_reserve.restype = ctypes.c_int
+lib.rq_pages_free.argtypes = [_p, _i32, _p, _p, _p, _p, _p]
+lib.rq_pages_free.restype = ctypes.c_int
+lib.rq_pages_compact.argtypes = [_p, _p, _p, _p, _p, _sz, _p]
+lib.rq_pages_compact.restype = ctypes.c_int
+_ropep = ctypes.POINTER(_rope_tensor)
+lib.rq_rope.argtypes = [ctypes.POINTER(rq_rope_config), _i32, _i32, _i32, _ropep, _ropep, _p, _p, _p]
+lib.rq_rope.restype = ctypes.c_int
 lib.rq_status_string.argtypes = [ctypes.c_int]
 lib.rq_status_string.restype = ctypes.c_char_p
 
@@ -192,3 +234,113 @@ def rq_decode_attention_bf16(k_cache, v_cache, k_cur, v_cur, q, seq_lens, batch,
         _ptr(k_cache), _ptr(v_cache), _ptr(k_cur), _ptr(v_cur), _ptr(q), _ptr(seq_lens), batch,
         num_heads, head_dim, max_seq, softmax_scale, _ptr(out), _ptr(workspace), workspace_bytes,
         _stream(stream)))
+
+
+def _arg(fn, x, dtypes, count=None):
+    """Address of x for a C call.  None and ints (device addresses) pass as they
+    are; a tensor has to be contiguous, of one of the dtypes (names), on the
+    device current on this thread and, where count is given, that long: a host
+    pointer or a short buffer would fault the device."""
+    if x is None or isinstance(x, int):
+        return x
+    import torch
+    if (not x.is_cuda or str(x.dtype).split(".")[1] not in dtypes or not x.is_contiguous()
+            or x.device.index != torch.cuda.current_device() or (count is not None and x.numel() < count)):
+        raise RqError(fn, 1)
+    return x.data_ptr()
+
+
+_I32, _BF16, _U64, _U8 = ("int32",), ("bfloat16",), ("int64", "uint64"), ("uint8",)
+
+
+def rq_tree_workspace_bytes(cfg: rq_config, batch: int, n_nodes: int) -> int:
+    return lib.rq_tree_workspace_bytes(ctypes.byref(cfg), batch, n_nodes)
+
+
+def rq_tree_attention(handle, layer, group, loop, batch, n_nodes, q, k_new, v_new, mask, node_counts, seq_lens,
+                      softmax_scale, out, workspace, workspace_bytes, stream=None):
+    """Attention of n_nodes drafted tokens per row (a tree, its visibility in mask)
+    over the cached tokens and the draft.  q, out: [batch, Hq, n_nodes, d] bf16;
+    k_new, v_new: [batch, H, n_nodes, d] bf16; mask: [batch, n_nodes,
+    ceil(n_nodes / 64)] int64 or uint64 bits, or None (a single sequence);
+    node_counts: [batch] int32 or None."""
+    fn = "rq_tree_attention"
+    _check(fn, lib.rq_tree_attention(
+        handle, layer, group, loop, batch, n_nodes, _arg(fn, q, _BF16), _arg(fn, k_new, _BF16),
+        _arg(fn, v_new, _BF16), _arg(fn, mask, _U64, batch * n_nodes * -(-n_nodes // 64)),
+        _arg(fn, node_counts, _I32, batch), _arg(fn, seq_lens, _I32, batch), softmax_scale, _arg(fn, out, _BF16),
+        _arg(fn, workspace, _U8, workspace_bytes), workspace_bytes, _stream(stream)))
+
+
+def rq_pages_workspace_bytes(cfg: rq_config, num_pages: int) -> int:
+    return lib.rq_pages_workspace_bytes(ctypes.byref(cfg), num_pages)
+
+
+def rq_pages_copy(handle, n, src, dst, status=None, stream=None):
+    """Copy page src[i] to page dst[i] of a paged cache, every layer and group."""
+    fn = "rq_pages_copy"
+    _check(fn, lib.rq_pages_copy(handle, n, _arg(fn, src, _I32, n), _arg(fn, dst, _I32, n),
+                                     _arg(fn, status, _I32, 4), _stream(stream)))
+
+
+def rq_pages_fork(handle, n, src_rows, dst_rows, refs, status=None, stream=None):
+    """Row dst_rows[i] shares the pages of row src_rows[i] and gives up its own."""
+    fn = "rq_pages_fork"
+    _check(fn, lib.rq_pages_fork(handle, n, _arg(fn, src_rows, _I32, n), _arg(fn, dst_rows, _I32, n),
+                                     _arg(fn, refs, _I32), _arg(fn, status, _I32, 4), _stream(stream)))
+
+
+def rq_pages_reserve(handle, batch, seq_lens, n_tokens, refs, status, workspace, workspace_bytes, stream=None):
+    """Give rows 0 .. batch-1 pages of their own for their next n_tokens positions
+    (copy on write where a page is shared)."""
+    fn = "rq_pages_reserve"
+    _check(fn, lib.rq_pages_reserve(handle, batch, _arg(fn, seq_lens, _I32, batch), n_tokens, _arg(fn, refs, _I32),
+                                        _arg(fn, status, _I32, 4), _arg(fn, workspace, _U8, workspace_bytes),
+                                        workspace_bytes, _stream(stream)))
+
+
+def rq_pages_free(handle, n, rows, keep, refs, status=None, stream=None):
+    """Give up the pages of rows[i] behind its first keep[i] tokens (keep None: all)."""
+    fn = "rq_pages_free"
+    _check(fn, lib.rq_pages_free(handle, n, _arg(fn, rows, _I32, n), _arg(fn, keep, _I32, n), _arg(fn, refs, _I32),
+                                     _arg(fn, status, _I32, 4), _stream(stream)))
+
+
+def rq_pages_compact(handle, refs, used, status, workspace, workspace_bytes, stream=None):
+    """Move the used pages to the front of the pool; used (int32 on the device)
+    receives their number."""
+    fn = "rq_pages_compact"
+    _check(fn, lib.rq_pages_compact(handle, _arg(fn, refs, _I32), _arg(fn, used, _I32, 1), _arg(fn, status, _I32, 4),
+                                        _arg(fn, workspace, _U8, workspace_bytes), workspace_bytes,
+                                        _stream(stream)))
+
+
+def rq_rope(cfg: rq_rope_config, q, k, start, offsets=None, q_out=None, k_out=None, stream=None):
+    """Rotate q and k ([batch, heads, n, d] tensors of any strides with contiguous
+    channels; either may be None) by positions start[b] + offsets[b, t] (offsets
+    None: + t).  q_out, k_out None: in place."""
+    import torch
+    fn = "rq_rope"
+    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    first = q if q is not None else k
+    if first is None or first.dim() != 4 or first.dtype not in code:
+        raise RqError(fn, 1)
+    batch, n = first.shape[0], first.shape[2]
+
+    def pack(x, y):
+        if x is None:
+            return None
+        y = x if y is None else y
+        for t in (x, y):
+            if (t.dim() != 4 or t.shape != x.shape or t.shape[0] != batch or t.shape[2] != n or t.dtype != first.dtype
+                    or t.shape[3] != cfg.head_dim or t.stride(3) != 1 or not t.is_cuda
+                    or t.device.index != torch.cuda.current_device()):
+                raise RqError(fn, 1)
+        return _rope_tensor(x.data_ptr(), y.data_ptr(), x.shape[1], x.stride(0), x.stride(1), x.stride(2),
+                            y.stride(0), y.stride(1), y.stride(2))
+
+    tq, tk = pack(q, q_out), pack(k, k_out)
+    _check(fn, lib.rq_rope(ctypes.byref(cfg), code[first.dtype], batch, n,
+                           ctypes.byref(tq) if tq is not None else None,
+                           ctypes.byref(tk) if tk is not None else None, _arg(fn, start, _I32, batch),
+                           _arg(fn, offsets, _I32, batch * n), _stream(stream)))

@@ -210,6 +210,36 @@ rq_status rq_decode_attention_append(rq_cache* cache, int32_t layer, int32_t gro
   return e == cudaSuccess ? RQ_OK : (e == cudaErrorNotSupported ? RQ_ERR_UNSUPPORTED : RQ_ERR_CUDA);
 }
 
+size_t rq_tree_workspace_bytes(const rq_config* cfg, int32_t batch, int32_t n_nodes) {
+  Geom g;
+  if (!cfg || !make_geom(*cfg, &g) || batch <= 0 || n_nodes <= 0 || n_nodes > RQ_MAX_TREE_NODES) return 0;
+  return tree_workspace_bytes(g, batch, n_nodes, current_sms());
+}
+
+rq_status rq_tree_attention(rq_cache* cache, int32_t layer, int32_t group, int32_t loop, int32_t batch,
+                            int32_t n_nodes, const void* q, const void* k_new, const void* v_new,
+                            const uint64_t* mask, const int32_t* node_counts, const int32_t* seq_lens,
+                            float softmax_scale, void* out, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  if (!cache || !q || !k_new || !v_new || !seq_lens || !out || !workspace) return RQ_ERR_INVALID_ARG;
+  if (!on_cache_device(*cache)) return RQ_ERR_INVALID_ARG;
+  const Geom& g = cache->geom;
+  if (layer < 0 || layer >= g.L || group < 0 || group >= g.G || loop < 0 || loop >= g.P || batch <= 0 ||
+      n_nodes <= 0)
+    return RQ_ERR_INVALID_ARG;
+  if (batch > g.Bmax) return RQ_ERR_CAPACITY;
+  if (batch > RQ_MAX_DECODE_BATCH || n_nodes > RQ_MAX_TREE_NODES) return RQ_ERR_UNSUPPORTED;
+  if (workspace_bytes < tree_workspace_bytes(g, batch, n_nodes, cache->num_sms)) return RQ_ERR_WORKSPACE;
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(mask) || !aligned16(node_counts) ||
+      !aligned16(seq_lens) || !aligned16(out) || !aligned16(workspace))
+    return RQ_ERR_ALIGNMENT;
+  cudaError_t e = launch_tree(*cache, layer, group, loop, batch, n_nodes, static_cast<const __nv_bfloat16*>(q),
+                              static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new),
+                              mask, node_counts, seq_lens, softmax_scale, static_cast<__nv_bfloat16*>(out),
+                              workspace, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RQ_OK : (e == cudaErrorNotSupported ? RQ_ERR_UNSUPPORTED : RQ_ERR_CUDA);
+}
+
 size_t rq_bf16_workspace_bytes(int32_t batch, int32_t num_heads, int32_t head_dim) {
   if (batch <= 0 || num_heads <= 0 || (head_dim != 96 && head_dim != 128)) return 0;
   return bf16_workspace_bytes(batch, num_heads, head_dim, current_sms());

@@ -92,6 +92,12 @@ cudaError_t launch_decode(const rq_cache& c, int layer, int group, int loop, int
                           float* out, void* workspace, cudaStream_t stream,
                           const __nv_bfloat16* kv_all = nullptr);
 
+size_t tree_workspace_bytes(const Geom& g, int batch, int n_nodes, int num_sms);
+cudaError_t launch_tree(const rq_cache& c, int layer, int group, int loop, int batch, int n_nodes,
+                        const __nv_bfloat16* q, const __nv_bfloat16* k_new, const __nv_bfloat16* v_new,
+                        const uint64_t* mask, const int32_t* counts, const int32_t* seq_lens, float scale,
+                        __nv_bfloat16* out, void* workspace, cudaStream_t stream);
+
 size_t bf16_workspace_bytes(int batch, int heads, int d, int num_sms);
 cudaError_t launch_bf16(const __nv_bfloat16* k, const __nv_bfloat16* v,
                         const __nv_bfloat16* k_cur, const __nv_bfloat16* v_cur,

@@ -44,7 +44,10 @@
  * rq_decode_attention_append (the anchor loop's attention plus the current
  * token's append); rq_decode_attention_noalloc (scratch inside the library);
  * rq_bf16_workspace_bytes / rq_decode_attention_bf16 (the uncompressed
- * comparator); rq_status_string.
+ * comparator); rq_tree_workspace_bytes / rq_tree_attention (several drafted
+ * tokens per row, each seeing its own ancestors); rq_pages_workspace_bytes and
+ * rq_pages_copy / _fork / _reserve / _free / _compact (page bookkeeping of the
+ * paged layout); rq_rope (rotary positions); rq_status_string.
  *
  * ---------------------------------------------------------------------------
  * Cache byte layout (this library's format; the pages fix the record
@@ -208,7 +211,8 @@ rq_status rq_append(rq_cache* cache, int32_t layer, int32_t group, int32_t batch
  * first use (the status word must start at zero).  Its first 16 bytes
  * are the status word (int32[4]): [0] != 0 after a device-side wait timed out,
  * [1] != 0 after an append skipped a row that would overflow, [2] != 0 after a
- * call met a block-table entry outside the page pool (paged layout). */
+ * call met a block-table entry outside the page pool (paged layout).  [3] is
+ * written by rq_pages_reserve only. */
 size_t rq_decode_workspace_bytes(const rq_config* cfg, int32_t batch);
 
 /* One decode-attention call: query loop `loop` (0-based; loop == P-1 is the
@@ -321,6 +325,187 @@ rq_status rq_decode_attention_bf16(const void* k_cache, const void* v_cache,
                                    int32_t head_dim, int32_t max_seq, float softmax_scale,
                                    float* out, void* workspace, size_t workspace_bytes,
                                    void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of a tree of drafted tokens
+ * --------------------------------------------------------------------------- */
+
+/* Drafted tokens per row that one rq_tree_attention call may cover. */
+#define RQ_MAX_TREE_NODES 256
+
+/* Workspace (device bytes) of one rq_tree_attention call for `batch` rows of
+ * n_nodes drafted tokens on the current device (0 if the shape is invalid).
+ * Zero-filled once before its first use; the first 16 bytes are the status
+ * word, as under rq_decode_workspace_bytes.  Calls that may run at the same
+ * time need a workspace each. */
+size_t rq_tree_workspace_bytes(const rq_config* cfg, int32_t batch, int32_t n_nodes);
+
+/* Attention of the drafted tokens of a speculative step: node t of row b
+ * attends, for query loop `loop` of (layer, group), the row's seq_lens[b]
+ * cached tokens (rebuilt for this loop, as rq_decode_attention does) and those
+ * drafted tokens of its row that its mask names, whose K/V of this loop are
+ * still in BF16.  A node sees itself only if its own bit is set.  The
+ * cache is only read; append the accepted path with rq_append afterwards.
+ *   n_nodes      T, drafted tokens per row: 1 .. RQ_MAX_TREE_NODES
+ *   q            device bf16 [batch][Hq][T][d]
+ *   k_new, v_new device bf16 [batch][H][T][d]: this loop's block of a
+ *                [P][2][batch][H][T][d] buffer, the layout that rq_append takes
+ *   mask         device uint64 [batch][T][ceil(T / 64)], or NULL: bit j % 64 of
+ *                word j / 64 of node t set = node t sees drafted token j.  Bits
+ *                at or behind the row's node count are ignored.  NULL: node t
+ *                sees drafted tokens 0 .. t (a single drafted sequence).
+ *   node_counts  device int32 [batch] or NULL: nodes in use per row (taken into
+ *                0 .. T); the output rows of nodes behind the count are not
+ *                written, their inputs do not enter any result (they may hold
+ *                anything).  NULL: T for every row.
+ *   seq_lens     device int32 [batch]
+ *   out          device bf16 [batch][Hq][T][d]; zero for a node that sees no key
+ * A K or V that a node's mask hides does not enter that node's result, not even
+ * when it is infinite or NaN.  q is scaled per node by a power of two and kept
+ * in 16-bit floating point (11 significant bits), as are the rebuilt K/V and the
+ * softmax weights; scores, softmax sums and accumulators are float32.
+ * With T = 1 and a mask that names the token itself this is
+ * rq_decode_attention with a BF16 result.
+ * Chained caches (RQ_MODE_CHAINED) are read as rq_decode_attention reads them.
+ * Errors: as rq_decode_attention; INVALID_ARG (n_nodes < 1), UNSUPPORTED
+ * (n_nodes > RQ_MAX_TREE_NODES, batch > RQ_MAX_DECODE_BATCH). */
+rq_status rq_tree_attention(rq_cache* cache, int32_t layer, int32_t group, int32_t loop,
+                            int32_t batch, int32_t n_nodes, const void* q, const void* k_new,
+                            const void* v_new, const uint64_t* mask, const int32_t* node_counts,
+                            const int32_t* seq_lens, float softmax_scale, void* out,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Pages of a paged cache
+ *
+ * Bookkeeping on the device, in stream order, for callers that branch rows
+ * (beams, parallel samples, drafted paths).  It uses the cache's block table
+ * (these calls write the table that rq_cache_create_paged was given) and one
+ * array the caller owns:
+ *   refs   device int32 [num_pages]: how many table entries name the page;
+ *          0 = free.  A caller that lets these calls do all its paging starts
+ *          with refs zero and every table entry -1 (no page).
+ * Rows that share a page (refs > 1) may all read it; before a row writes to it
+ * (rq_append, rq_decode_attention_append), rq_pages_reserve gives the row a page
+ * of its own.  Table entries outside [0, num_pages) name no page; none of these
+ * calls follows one.
+ *   status device int32[4] or NULL: [1] = 1 after a row was skipped, [2] = 1
+ *          after a page pair was skipped, [3] = 1 when the free pages ran out.
+ * A call on a cache of the contiguous layout returns RQ_ERR_INVALID_ARG.  All
+ * other errors: INVALID_ARG (null, negative count), CAPACITY (more rows than
+ * max_batch, n_tokens > max_seq_len), ALIGNMENT, WORKSPACE, CUDA.
+ * --------------------------------------------------------------------------- */
+
+/* Workspace (device bytes) of rq_pages_reserve and rq_pages_compact for caches
+ * of this shape with num_pages pages; needs no initial value.  0 if invalid. */
+size_t rq_pages_workspace_bytes(const rq_config* cfg, int32_t num_pages);
+
+/* Copy page src[i] to page dst[i], in every layer and group, i < n.  Table and
+ * counts are not touched.  A pair is skipped (status [2]) when a page is outside
+ * the pool, when dst[i] is the source of another pair, or when an earlier pair
+ * has the same dst; src[i] == dst[i] does nothing.
+ *   src, dst   device int32 [n], 16-byte aligned; n <= num_pages (CAPACITY) */
+rq_status rq_pages_copy(rq_cache* cache, int32_t n, const int32_t* src, const int32_t* dst,
+                        int32_t* status, void* stream);
+
+/* Row dst_rows[i] takes the pages of row src_rows[i] (shared, no bytes are
+ * copied) and gives up its own, i < n: all sources are read before any row is
+ * changed, so a permutation of beams is one call.  A dst row named twice takes
+ * the last pair's source.  A row index outside [0, max_batch) skips its pair
+ * (status [1]).  The caller moves the rows' lengths.
+ *   src_rows, dst_rows  device int32 [n], n <= max_batch; more than 6144 pairs:
+ *                       UNSUPPORTED */
+rq_status rq_pages_fork(rq_cache* cache, int32_t n, const int32_t* src_rows, const int32_t* dst_rows,
+                        int32_t* refs, int32_t* status, void* stream);
+
+/* Make the tiles of positions seq_lens[b] .. seq_lens[b] + n_tokens - 1 of rows
+ * 0 .. batch-1 writable: an entry that names no page gets a free page; a page
+ * that other entries share is replaced by a free page, which receives a copy of
+ * its bytes when the tile already holds tokens of the row (copy on write).  When
+ * every holder of a page asks in one call, the last of them keeps it.  Requests are
+ * served in row, then tile order, from the lowest free page up.  Where the free
+ * pages run out an entry stays as it is (status [3]).  A row with a negative
+ * length or seq_lens[b] + n_tokens > max_seq_len is skipped (status [1]).  n_tokens = 0 does
+ * nothing. */
+rq_status rq_pages_reserve(rq_cache* cache, int32_t batch, const int32_t* seq_lens, int32_t n_tokens,
+                           int32_t* refs, int32_t* status, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Give up the tiles of rows[i] at or behind token keep[i] (tiles that hold none
+ * of the first keep[i] tokens), i < n: their entries become -1 and their pages
+ * lose one holder.  keep NULL: the whole row.  A row named twice loses what any
+ * of its pairs gives up.  A row index outside [0, max_batch) is skipped (status [1]).
+ *   rows, keep   device int32 [n] */
+rq_status rq_pages_free(rq_cache* cache, int32_t n, const int32_t* rows, const int32_t* keep,
+                        int32_t* refs, int32_t* status, void* stream);
+
+/* Move pages so that the used ones are 0 .. used-1: the i-th free page below
+ * `used` takes the bytes, the count and the table entries of the i-th used page at or above it.
+ *   used   device int32, receives the number of pages with refs > 0 */
+rq_status rq_pages_compact(rq_cache* cache, int32_t* refs, int32_t* used, int32_t* status,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions
+ * --------------------------------------------------------------------------- */
+
+typedef enum rq_dtype { RQ_BF16 = 0, RQ_F16 = 1, RQ_F32 = 2 } rq_dtype;
+
+typedef enum rq_rope_scaling {
+  RQ_ROPE_PLAIN = 0,    /* f_i = theta^(-2i / rotary_dim) */
+  RQ_ROPE_LINEAR = 1,   /* f_i / factor: positions squeezed by `factor` */
+  RQ_ROPE_BASE = 2,     /* theta replaced by theta * factor^(r / (r - 2)): the slowest frequency
+                           is divided by `factor`, the fastest stays */
+  RQ_ROPE_PARTS = 3     /* f_i (k_i + (1 - k_i) / factor), k_i = clamp((u_i - low_turns) /
+                           (high_turns - low_turns), 0, 1), u_i = original_len f_i / 2pi: the turns
+                           that pair i makes over the original length */
+} rq_rope_scaling;
+
+/* How rq_rope turns a head. */
+typedef struct rq_rope_config {
+  int32_t head_dim;      /* channels per head, 2 .. 512 */
+  int32_t rotary_dim;    /* r: the first r channels are rotated (even, 2 .. min(head_dim, 256)); the
+                            others are copied */
+  int32_t interleaved;   /* 0: channel i pairs with i + r/2; 1: channel 2i pairs with 2i + 1 */
+  int32_t inverse;       /* 1: rotate by the negative angle.  The map is linear and this is its
+                            transpose: out = gradient of in for in = gradient of out */
+  int32_t scaling;       /* rq_rope_scaling */
+  int32_t original_len;  /* RQ_ROPE_PARTS: context the model was trained for */
+  double theta;          /* > 1, e.g. 10000 */
+  double factor;         /* > 0; not used by RQ_ROPE_PLAIN */
+  double low_turns, high_turns;   /* RQ_ROPE_PARTS: low < high */
+  double magnitude;      /* the rotated channels are multiplied by it (0 counts as 1) */
+} rq_rope_config;
+
+/* One tensor [batch][heads][n][d] read and written by rq_rope: the element
+ * strides of row, head and token; channels are contiguous.  Any strides do;
+ * pointers and strides that are multiples of 16 bytes are faster.  out may be
+ * in (with the same strides); otherwise the two must not overlap. */
+typedef struct rq_rope_tensor {
+  const void* in;
+  void* out;
+  int32_t heads;
+  int64_t in_row, in_head, in_token;
+  int64_t out_row, out_head, out_token;
+} rq_rope_tensor;
+
+/* Rotate queries and keys by their positions: pair (a, b) of frequency i becomes
+ * magnitude * (a cos - b sin, b cos + a sin) at angle position * f_i.  Positions
+ * are start[b] + offsets[b][t], offsets NULL: start[b] + t, so with start =
+ * seq_lens a prompt, a decoded token (n = 1) or the nodes of a drafted tree
+ * (offsets = their depths) sit where they belong.  Angles are taken modulo a
+ * turn in 64-bit fixed point: exact for every int32 position.  Arithmetic is
+ * float32, rounded once to the tensors' type.
+ *   dtype    rq_dtype of every tensor
+ *   q, k     host; k (or q) may be NULL
+ *   start    device int32 [batch], or NULL: zeros
+ *   offsets  device int32 [batch][n] or NULL
+ * The tensors need only be aligned to their element.
+ * Errors: INVALID_ARG (null, bad count or config), ALIGNMENT, UNSUPPORTED
+ * (head_dim or rotary_dim outside the ranges, heads x batch > 2^30), CUDA. */
+rq_status rq_rope(const rq_rope_config* cfg, int32_t dtype, int32_t batch, int32_t n,
+                  const rq_rope_tensor* q, const rq_rope_tensor* k, const int32_t* start,
+                  const int32_t* offsets, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* rq_status_string(rq_status status);
