@@ -8,37 +8,14 @@
 // dequantized residual), so with R applied once to the query and once to the sum
 //   q . k = c (q . a) + (R q) . r,    sum p v = sum (p c) a + R^T sum p r;
 // chained caches fold the planes from the anchor down: x <- c_j x + (R q) . r_j.
-#include <cuda_fp8.h>
-
-#include "rq_internal.cuh"
+#include "rq_tree_kernels.cuh"
 
 namespace rq {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct TreeArgs {
-  Geom g;
-  const uint8_t* base;
-  const float* R;
-  const __nv_bfloat16 *q, *k_new, *v_new;
-  const unsigned long long* mask;
-  const int32_t *counts, *seq_lens;
-  __nv_bfloat16* out;
-  int32_t* status;
-  int layer, group, batch, T, words, loop, nres;
-  float qscale;                    // softmax_scale * log2(e)
-};
-
 __device__ __forceinline__ float2 meta2(const uint8_t* p) {   // (scale, offset)
   return e4m3x2_to_f32x2(*reinterpret_cast<const uint16_t*>(p));
 }
-__device__ __forceinline__ int clamp_len(int n, int nmax) { return n < 0 ? 0 : (n > nmax ? nmax : n); }
-__device__ __forceinline__ bool sees(const TreeArgs& a, int b, int t, int j) {
-  if (!a.mask) return j <= t;
-  return (__ldg(a.mask + ((size_t)b * a.T + t) * a.words + (j >> 6)) >> (j & 63)) & 1u;
-}
-
 // ---- one CTA per (node, query head, row) -------------------------------------
 // Dequantizes every key and value for its one query: the CTAs of one KV head read
 // the same tiles from L2.  Bound by that arithmetic, not by memory.
@@ -214,16 +191,34 @@ __global__ void __launch_bounds__(kRowThreads) tree_row_kernel(TreeArgs a) {
 
 }  // namespace
 
+// Queries per block: the smallest operand width that holds a KV head's M queries, 64 at most
+static int tree_nb(int M) { return M <= 16 ? 16 : (M <= 32 ? 32 : 64); }
+
+namespace {
+struct TreeSpace {
+  size_t partials, scales, packs, total;   // byte offsets
+};
+TreeSpace tree_space(const Geom& g, int batch, int n_nodes, int num_sms) {
+  TreeSpace w = {256, 256, 256, 256};
+  if (g.mode & RQ_MODE_CHAINED) return w;
+  const int M = g.qpk * n_nodes, nb = tree_nb(M), planes = g.P > 1 ? 2 : 1;
+  const size_t units = (size_t)batch * g.H * ((M + nb - 1) / nb);
+  w.scales = w.partials + (units + num_sms) * (size_t)(2 * nb + planes * nb * g.d) * sizeof(float);
+  w.packs = (w.scales + units * nb * sizeof(float) + 255) / 256 * 256;
+  w.total = w.packs + units * planes * 2 * nb * 128;
+  return w;
+}
+}  // namespace
+
 size_t tree_workspace_bytes(const Geom& g, int batch, int n_nodes, int num_sms) {
-  (void)g; (void)batch; (void)n_nodes; (void)num_sms;
-  return 256;
+  return tree_space(g, batch, n_nodes, num_sms).total;
 }
 
 cudaError_t launch_tree(const rq_cache& c, int layer, int group, int loop, int batch, int n_nodes,
                         const __nv_bfloat16* q, const __nv_bfloat16* k_new, const __nv_bfloat16* v_new,
                         const uint64_t* mask, const int32_t* counts, const int32_t* seq_lens, float scale,
                         __nv_bfloat16* out, void* workspace, cudaStream_t stream) {
-  TreeArgs a;
+  TreeArgs a = {};
   a.g = c.geom;
   a.base = c.base;
   a.R = c.R;
@@ -244,9 +239,24 @@ cudaError_t launch_tree(const rq_cache& c, int layer, int group, int loop, int b
   const bool chained = (c.geom.mode & RQ_MODE_CHAINED) != 0;
   a.nres = loop == c.geom.P - 1 ? 0 : (chained ? c.geom.P - 1 - loop : 1);
   a.qscale = scale * kLog2e;
+  if (!chained) {
+    const int nb = tree_nb(c.geom.qpk * n_nodes);
+    const TreeSpace w = tree_space(c.geom, batch, n_nodes, c.num_sms);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.M = c.geom.qpk * n_nodes;
+    a.nqb = (a.M + nb - 1) / nb;
+    a.partials = reinterpret_cast<float*>(ws + w.partials);
+    a.q_scale = reinterpret_cast<float*>(ws + w.scales);
+    a.packs = ws + w.packs;
+    return c.geom.d == 128 ? launch_tree_mma(a, nb, c.num_sms, stream) : launch_tree_mma_96(a, nb, c.num_sms, stream);
+  }
   if (c.geom.Hq > 65535) return cudaErrorNotSupported;   // grid.y
   tree_row_kernel<<<dim3(n_nodes, c.geom.Hq, batch), kRowThreads, 0, stream>>>(a);
   return cudaGetLastError();
+}
+
+cudaError_t launch_tree_mma(const TreeArgs& a, int nb, int num_sms, cudaStream_t stream) {
+  return launch_tree_d<128>(a, nb, num_sms, stream);
 }
 
 }  // namespace rq

@@ -1,0 +1,1205 @@
+// The tensor-core path of rq_tree_attention (shared-anchor caches): query prep, the
+// streaming kernel, the merge.  rq_tree.cu has the mathematics and the choice of path.
+//
+// Work unit: the queries of one (row, KV head) -- T nodes times the Hq / H query heads
+// that share the head, consecutive rows of q -- in blocks of NB = 16, 32 or 64, times
+// the head's cached tokens in steps of 128.  The steps of all units are dealt out evenly
+// to a persistent grid of one CTA per SM; a CTA leaves one partial softmax state
+// (m, l, O) per unit it touched, and the merge joins them.
+//
+// Per step, transposed products keep the padding off the queries' side: the 128-row
+// operand is made of cache data, the N side is the NB queries.
+//   scores  S^T [128 tokens x NB] = K' Q'^T     (anchor and residual part apart:
+//                                                s = c Sa + Sr, c in the token's lane)
+//   values  O^T [channels x NB] += V'^T P^T     (anchor and residual part apart)
+// K' and V'^T are dequantized into registers and stored to tensor memory as the A operand
+// (f16, one token or channel per lane): dequantized data never touches shared memory.
+// Roles (14 warps): K dequantizer, softmax, V dequantizer (4 warps each, one per 32
+// lanes), one copy warp, one MMA warp.
+//
+// Dequantization: a code moved into the mantissa of 16.0 (INT4) or 4.0 (INT2) is the
+// exact f16 16 + code; one fused multiply-add with (s, o - 16 s) gives s code + o rounded
+// once: shift, mask, multiply-add per two elements.
+//
+// Softmax: a token's scores sit in one lane, a query's across the lanes.  The running
+// reference of a query therefore moves only when some score exceeds it by 2^8 (the first
+// step, then rarely): weights stay below 2^14, in f16 range, and O is rescaled in
+// tensor memory then.  Sums stay in the lanes' registers until the unit ends.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "rq_internal.cuh"
+
+namespace rq {
+
+struct TreeArgs {
+  Geom g;
+  const uint8_t* base;
+  const float* R;
+  const __nv_bfloat16 *q, *k_new, *v_new;
+  const unsigned long long* mask;
+  const int32_t *counts, *seq_lens;
+  __nv_bfloat16* out;
+  int32_t* status;
+  int layer, group, batch, T, words, loop, nres;
+  float qscale;                    // softmax_scale * log2(e)
+  // tensor-core path
+  int M, nqb;                      // queries per (row, KV head); blocks of NB of them
+  float* partials;                 // [num CTAs + units][pstride]
+  uint8_t* packs;                  // [units][image]: query operands
+  float* q_scale;                  // [units][NB]: factor from a score product to log2 units
+  int64_t pstride;
+};
+
+cudaError_t launch_tree_mma(const TreeArgs& a, int nb, int num_sms, cudaStream_t stream);
+cudaError_t launch_tree_mma_96(const TreeArgs& a, int nb, int num_sms, cudaStream_t stream);
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTreeStep = 128;               // tokens per step: two layout tiles
+constexpr int kTreeThreads = 14 * 32;
+constexpr int kTreeRows = RQ_MAX_DECODE_BATCH;
+constexpr int kMergeQ = 8;                   // queries per merge CTA
+constexpr int kPrepQ = 8;                    // queries per prep CTA
+constexpr float kHead = 6.f;                 // a row maximum's weight is 2^kHead
+constexpr float kTop = 14.f;                 // largest log2 weight before the reference moves
+
+__device__ __forceinline__ int clamp_len(int n, int nmax) { return n < 0 ? 0 : (n > nmax ? nmax : n); }
+__device__ __forceinline__ bool sees(const TreeArgs& a, int b, int t, int j) {
+  if (!a.mask) return j <= t;
+  return (__ldg(a.mask + ((size_t)b * a.T + t) * a.words + (j >> 6)) >> (j & 63)) & 1u;
+}
+
+struct TreeSplit {
+  int q, rem;
+  __device__ __forceinline__ int start(int c) const { return c * q + min(c, rem); }
+  __device__ __forceinline__ int owner(int u) const {
+    const int big = (q + 1) * rem;
+    return u < big ? u / (q + 1) : rem + (u - big) / q;
+  }
+};
+
+// ---- tcgen05 ---------------------------------------------------------------------
+__device__ __forceinline__ void tc_alloc(uint32_t* slot, int cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+               : "memory");
+}
+__device__ __forceinline__ void tc_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tc_dealloc(uint32_t addr, int cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// D[128 x N] (+)= A[128 x 16] B[16 x N]: A in tensor memory, B in shared memory
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+// f16 x f16 -> f32 products of 128 rows and n columns; b_mn: B's columns contiguous
+constexpr uint32_t tc_idesc(int n, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n / 8) << 17) | ((128u / 16) << 24);
+}
+// Shared-memory operand in 128-byte rows, 8-row groups 1024 bytes apart, 128-byte swizzle
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(1024 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 |
+         2ull << 61;
+}
+// Named barrier of one warpgroup; wg_any: true when any thread's predicate holds.
+__device__ __forceinline__ void wg_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool wg_any(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)p)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ---- f16 pairs ---------------------------------------------------------------------
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ __half2 e4m3_pair(uint16_t v) {   // (scale, offset), exact
+  uint32_t h2;
+  asm("{\n\t.reg .b16 t;\n\tmov.b16 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h2) : "h"(v));
+  return u2h(h2);
+}
+__device__ __forceinline__ __half half_sat(float x) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.f), "f"(x));
+  return __low2half(u2h(r));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+// two f32 -> f16x2, lo in the low half; no saturation: infinities stay
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// INT4 word: r[s] = (16 + code at bits 4s, 16 + code at bits 4s + 16)
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t (&r)[4]) {
+  r[0] = ((w << 6) & 0x03C003C0u) | 0x4C004C00u;
+  r[1] = ((w << 2) & 0x03C003C0u) | 0x4C004C00u;
+  r[2] = ((w >> 2) & 0x03C003C0u) | 0x4C004C00u;
+  r[3] = ((w >> 6) & 0x03C003C0u) | 0x4C004C00u;
+}
+// INT2 word: r[4 i + m] = (4 + code at bits 8 i + 2 m, 4 + code at bits 8 i + 2 m + 16), i = 0, 1
+__device__ __forceinline__ void codes2(uint32_t w, uint32_t (&r)[8]) {
+  r[0] = ((w << 8) & 0x03000300u) | 0x44004400u;
+  r[1] = ((w << 6) & 0x03000300u) | 0x44004400u;
+  r[2] = ((w << 4) & 0x03000300u) | 0x44004400u;
+  r[3] = ((w << 2) & 0x03000300u) | 0x44004400u;
+  r[4] = (w & 0x03000300u) | 0x44004400u;
+  r[5] = ((w >> 2) & 0x03000300u) | 0x44004400u;
+  r[6] = ((w >> 4) & 0x03000300u) | 0x44004400u;
+  r[7] = ((w >> 6) & 0x03000300u) | 0x44004400u;
+}
+// Per-CTA view of the call's work, in shared memory: steps before row b, steps of a unit of row b
+struct TreeRowsShared {
+  int pre[kTreeRows + 1];
+  int len[kTreeRows];
+};
+// Fills it (first warp; every thread of the CTA then synchronizes); units_per_row = H * nqb.
+__device__ __forceinline__ void tree_rows(const TreeArgs& a, TreeRowsShared* s) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, per = a.g.H * a.nqb;
+    int run = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const int b = b0 + lane;
+      const int n = b < a.batch ? clamp_len(a.seq_lens[b], a.g.Nmax) : 0;
+      if (b < a.batch) s->len[b] = n;
+      int x = (n + kTreeStep - 1) / kTreeStep * per;
+      const int own = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (b < a.batch) s->pre[b] = run + x - own;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) s->pre[a.batch] = run;
+  }
+}
+
+// A position in the sequence of steps
+struct TreeCursor {
+  int b, in_row, step, steps;       // row, unit within the row, step of the unit, its steps
+  __device__ __forceinline__ void seek(const TreeRowsShared& s, int batch, int u) {
+    int lo = 0, hi = batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.pre[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    steps = (s.len[b] + kTreeStep - 1) / kTreeStep;
+    const int rem = u - s.pre[b];
+    in_row = rem / steps;
+    step = rem % steps;
+  }
+  // to the next step (there is one); per: units per row
+  __device__ __forceinline__ void next(const TreeRowsShared& s, int per) {
+    if (++step < steps) return;
+    step = 0;
+    if (++in_row < per) return;
+    in_row = 0;
+    do {
+      ++b;
+      steps = (s.len[b] + kTreeStep - 1) / kTreeStep;
+    } while (steps == 0);
+  }
+};
+
+template <int D, int GS, int NRES, int NB>
+struct TreeCfg {
+  static constexpr int NG = D / GS;
+  static constexpr int A_CODES = kTile * D / 2, R_CODES = kTile * D / 4, META = kTile * NG * 2;
+  static constexpr int A_TILE = A_CODES + META, R_TILE = R_CODES + META + kTile * 2;
+  // stage: K anchor, V anchor, K residual, V residual, two tiles each
+  static constexpr int AV = 2 * A_TILE, RK = 4 * A_TILE, RV = 4 * A_TILE + 2 * R_TILE;
+  static constexpr int STAGE = 4 * A_TILE + NRES * 4 * R_TILE;
+  static constexpr int PL = 1 + NRES;
+  static constexpr int QBLK = NB * 128;                    // 64 channels of all queries
+  static constexpr int IMG = PL * 2 * QBLK;                // query operand of a unit
+  static constexpr int PBUF = kTreeStep * 128;             // weights: 128-byte row per token
+  static constexpr int TAB = PL * NG * 64 * 8 + NRES * 256; // V constants
+  static constexpr int FIX = 2 * IMG + 2 * PBUF + TAB;
+  static constexpr int STAGES = FIX + 4 * STAGE + 6144 <= 226 * 1024 ? 4 : 3;
+  static constexpr int SMEM = FIX + STAGES * STAGE + 1024;
+  static constexpr int SBUF = NB <= 32 ? 2 : 1;
+  // tensor memory columns
+  static constexpr int KA = 0, KR = 64, VA = 128, VR = 192, OA = 256, OR = 256 + NB, S0 = 256 + 2 * NB;
+  static constexpr int SCOLS = 2 * NB;                     // Sa, Sr
+  static_assert(S0 + SBUF * SCOLS <= 512, "tensor memory");
+  static_assert(SMEM <= 227 * 1024 - 5120, "shared memory");
+  // floats of a partial: m[NB], l[NB], O as [plane][NB/4][D][4]
+  static constexpr int PSTRIDE = 2 * NB + PL * NB * D;
+};
+
+// ---- query prep --------------------------------------------------------------------
+// One CTA per kPrepQ queries of a unit: x and R x as f16 times a power of two of the
+// query's own (its largest component to 2^10 .. 2^11: R keeps norms, so both stay below
+// 2^15), in the layout of the B operand.
+template <int D, int NRES, int NB>
+__global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
+  constexpr int RPW = D / 8;
+  constexpr int PL = 1 + NRES;
+  constexpr int IMG = PL * 2 * NB * 128;
+  __shared__ __align__(16) float q_s[kPrepQ][128];
+  __shared__ float r_s[kPrepQ][128];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int unit = blockIdx.x / (NB / kPrepQ), q0 = blockIdx.x % (NB / kPrepQ) * kPrepQ;
+  const int qb = unit % a.nqb, bh = unit / a.nqb, b = bh / a.g.H;
+  const bool hadamard = (a.g.mode & RQ_MODE_HADAMARD) != 0;
+  float4 rv[NRES ? RPW : 1];
+  if (NRES && !hadamard) {   // R does not change while the cache is used: before the wait
+#pragma unroll
+    for (int v = 0; v < RPW; ++v)
+      rv[v] = lane < D / 4 ? __ldg(reinterpret_cast<const float4*>(a.R + (size_t)(warp + 8 * v) * D) + lane)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  pdl_wait();
+  pdl_launch_dependents();   // what ran before the call is complete: the next kernel may read the cache
+  const int cnt = a.counts ? clamp_len(a.counts[b], a.T) : a.T;
+  const __nv_bfloat16* qu = a.q + ((size_t)bh * a.M + (size_t)qb * NB) * D;
+  const int rows = min(NB, a.M - qb * NB);
+  {   // one warp per query; a query that is not finite keeps the scale 1 and stays so
+    const int r = q0 + warp;
+    const bool on = r < rows && (qb * NB + r) % a.T < cnt;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (on && lane < D / 4) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(qu + (size_t)r * D) + lane);
+      x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+      x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    }
+    float big = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    int e = 11;
+    if (big > 0.f && isfinite(big)) frexpf(big, &e);   // big = f 2^e, f in [0.5, 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (lane < D / 4) q_s[warp][4 * lane + i] = ldexpf(x[i], 11 - e);
+    if (lane == 0) a.q_scale[(size_t)unit * NB + r] = ldexpf(a.qscale, e - 11);
+  }
+  __syncthreads();
+  if (NRES && hadamard) {
+    // one warp per query: lane holds channels lane, lane + 32, ...; stages h = 1 .. 64
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = q_s[warp][(lane + 32 * i) % D];
+#pragma unroll
+    for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float p = __shfl_xor_sync(0xffffffffu, v[i], h);
+        v[i] = (lane & h) ? p - v[i] : v[i] + p;
+      }
+    const float s0 = v[0] + v[1], s1 = v[0] - v[1], s2 = v[2] + v[3], s3 = v[2] - v[3];
+    if (D == 128) {
+      r_s[warp][lane] = (s0 + s2) * kInvSqrt128;
+      r_s[warp][lane + 32] = (s1 + s3) * kInvSqrt128;
+      r_s[warp][lane + 64] = (s0 - s2) * kInvSqrt128;
+      r_s[warp][lane + 96] = (s1 - s3) * kInvSqrt128;
+    }
+    __syncthreads();
+  } else if (NRES) {
+    // (R x)[row]: lane partials of the warp's rows, then a reduce-scatter over the lanes
+    for (int qi = 0; qi < kPrepQ; ++qi) {
+      const float4 x = lane < D / 4 ? reinterpret_cast<const float4*>(q_s[qi])[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+      float pv[16];
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        pv[v] = v < RPW ? fmaf(rv[v].x, x.x, fmaf(rv[v].y, x.y, fmaf(rv[v].z, x.z, rv[v].w * x.w))) : 0.f;
+#pragma unroll
+      for (int o = 16, n = 8; n >= 1; o >>= 1, n >>= 1) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          const float send = up ? pv[i] : pv[i + n], keep = up ? pv[i + n] : pv[i];
+          pv[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+      }
+      pv[0] += __shfl_xor_sync(0xffffffffu, pv[0], 1);
+      const int row = warp + 8 * (lane >> 1);
+      if ((lane & 1) == 0 && row < D) r_s[qi][row] = pv[0];
+    }
+    __syncthreads();
+  }
+  // the operand: 8 channels (16 bytes) a thread, rows of 64 channels, swizzled
+  uint8_t* img = a.packs + (size_t)unit * IMG;
+  for (int i = tid; i < PL * kPrepQ * (D / 8); i += 256) {
+    const int c = i % (D / 8), qi = i / (D / 8) % kPrepQ, pl = i / (D / 8 * kPrepQ);
+    const float* x = pl ? r_s[qi] : q_s[qi];
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {   // slots 8 c + 2 j, + 1
+      const int lo = pl ? (c >> 1) * 16 + (c & 1) * 4 + j : c * 8 + j;
+      w[j] = f16x2(x[lo], x[lo + (pl ? 8 : 4)]);
+    }
+    const int r = q0 + qi, kb = c >> 3, chunk = c & 7;
+    *reinterpret_cast<uint4*>(img + (pl * 2 + kb) * (NB * 128) + r * 128 + ((chunk ^ (r & 7)) << 4)) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ---- the streaming kernel --------------------------------------------------------
+template <int D, int GS, int NRES, int NB>
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
+  using C = TreeCfg<D, GS, NRES, NB>;
+  constexpr int ST = C::STAGES, NG = C::NG, PL = C::PL, SB = C::SBUF;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full_bar[ST], empty_bar[ST], qfull_bar[2], qempty_bar[2], kfull_bar[2], kempty_bar[2],
+      vfull_bar[2], vempty_bar[2], sfull_bar[2], sempty_bar[2], pfull_bar[2], pempty_bar[2], drain_bar;
+  __shared__ TreeRowsShared rows_s;
+  __shared__ __align__(16) float qm_s[NB / 2][4];   // two queries: their scales, minus their references
+  __shared__ __align__(16) float f_s[NB];
+  __shared__ float wred_s[4][NB];
+  __shared__ uint32_t tmem_s;
+  __shared__ volatile int abort_s;
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* q_img = smem;                                  // two query operands
+  uint8_t* p_buf = q_img + 2 * C::IMG;                    // two weight buffers
+  uint8_t* stages = p_buf + 2 * C::PBUF;
+  uint8_t* tab = stages + ST * C::STAGE;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = a.g.H * a.nqb;
+
+  tree_rows(a, &rows_s);
+  if (tid == 32) {
+    for (int i = 0; i < ST; ++i) { mbar_init(&full_bar[i], 1); mbar_init(&empty_bar[i], NRES ? 12 : 8); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&qfull_bar[i], 1); mbar_init(&qempty_bar[i], 1);
+      mbar_init(&kfull_bar[i], 4); mbar_init(&kempty_bar[i], 1);
+      mbar_init(&vfull_bar[i], 4); mbar_init(&vempty_bar[i], 1);
+      mbar_init(&sfull_bar[i], 1); mbar_init(&sempty_bar[i], 4);
+      mbar_init(&pfull_bar[i], 4); mbar_init(&pempty_bar[i], 1);
+    }
+    mbar_init(&drain_bar, 1);
+    abort_s = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int U = rows_s.pre[a.batch];
+  const TreeSplit split{U / (int)gridDim.x, U % (int)gridDim.x};
+  const int u0 = split.start(blockIdx.x), n_it = split.start(blockIdx.x + 1) - u0;
+  if (n_it <= 0) {
+    pdl_launch_dependents();
+    pdl_wait();
+    return;
+  }
+  if (warp == 13) {
+    tc_alloc(&tmem_s, 512);
+    tc_relinquish();
+    tc_before();
+  }
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = tmem_s;
+  pdl_launch_dependents();
+
+  // Waits are bounded.  Past the limit the CTA gives up: the copy and the MMA warp stop
+  // and let what they issued finish; the other roles run on to their end without
+  // waiting (their warps share named barriers, so none may leave alone).
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    while (!abort_s) {
+      if (mbar_try_wait_sleep(bar, parity)) return true;
+      if (global_ns() - t0 > kWaitNs) {
+        abort_s = 1;
+        atomicExch(&a.status[0], 1);
+      }
+    }
+    return false;
+  };
+  // the same by a whole warp, which goes on together (the tcgen05 loads and stores are warp-wide)
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    (void)wait(bar, parity);
+    __syncwarp();
+  };
+  // the step's tokens in the cache, all warps agree
+  auto valid_of = [&](const TreeCursor& c) { return min(kTreeStep, rows_s.len[c.b] - c.step * kTreeStep); };
+
+  TreeCursor cur;
+  cur.seek(rows_s, a.batch, u0);
+
+  if (warp == 12) {
+    // ================= copies =================
+    if (lane == 0) {
+      const uint64_t pol = l2_evict_first_policy();
+      int seg = 0, issued = 0;
+      bool waited = false, ok = true;
+      auto load_q = [&](int unit) {
+        uint64_t* bar = &qfull_bar[seg & 1];
+        if (!(ok = wait(&qempty_bar[seg & 1], ((seg >> 1) & 1) ^ 1))) return;
+        mbar_arrive_expect_tx(bar, C::IMG);
+        bulk_g2s(q_img + (seg & 1) * C::IMG, a.packs + (size_t)unit * C::IMG, C::IMG, bar);
+        ++seg;
+      };
+      int pend_unit = -1;     // units whose operand waits for the prep kernel
+      for (int it = 0; it < n_it && ok; ++it) {
+        const int st = it % ST;
+        if (!(ok = wait(&empty_bar[st], ((it / ST) & 1) ^ 1))) break;
+        const int h = cur.in_row / a.nqb;
+        const int tiles = (valid_of(cur) + kTile - 1) / kTile, t0 = cur.step * 2;
+        uint8_t* dst = stages + st * C::STAGE;
+        mbar_arrive_expect_tx(&full_bar[st], tiles * (2 * C::A_TILE + NRES * 2 * C::R_TILE));
+        if (!a.g.paged) {      // the two tiles of a plane are neighbours
+          for (int kv = 0; kv < 2; ++kv) {
+            bulk_g2s_hint(dst + kv * C::AV, a.base + a.g.tile_offset(a.layer, a.group, cur.b, h, true, 0, kv, t0, 0),
+                          tiles * C::A_TILE, &full_bar[st], pol);
+            if (NRES)
+              bulk_g2s_hint(dst + (kv ? C::RV : C::RK),
+                            a.base + a.g.tile_offset(a.layer, a.group, cur.b, h, false, a.loop, kv, t0, 0),
+                            tiles * C::R_TILE, &full_bar[st], pol);
+          }
+        } else {
+          for (int i = 0; i < tiles; ++i) {
+            int page = checked_page(a.g, raw_page(a.g, cur.b, t0 + i), a.status);
+            if (page < 0) page = 0;
+            for (int kv = 0; kv < 2; ++kv) {
+              bulk_g2s_hint(dst + kv * C::AV + i * C::A_TILE,
+                            a.base + a.g.tile_offset(a.layer, a.group, cur.b, h, true, 0, kv, t0 + i, page), C::A_TILE,
+                            &full_bar[st], pol);
+              if (NRES)
+                bulk_g2s_hint(dst + (kv ? C::RV : C::RK) + i * C::R_TILE,
+                              a.base + a.g.tile_offset(a.layer, a.group, cur.b, h, false, a.loop, kv, t0 + i, page),
+                              C::R_TILE, &full_bar[st], pol);
+            }
+          }
+        }
+        ++issued;
+        if (it == 0 || cur.step == 0) {
+          const int unit = cur.b * per + cur.in_row;
+          if (!waited && it == 0 && n_it > 1 && cur.step + 1 < cur.steps && ST > 1) {
+            pend_unit = unit;    // one more step of the cache first: the prep kernel may still run
+          } else {
+            if (!waited) { pdl_wait(); waited = true; }
+            if (pend_unit >= 0) { load_q(pend_unit); pend_unit = -1; if (!ok) break; }
+            load_q(unit);
+          }
+        } else if (pend_unit >= 0) {
+          if (!waited) { pdl_wait(); waited = true; }
+          load_q(pend_unit);
+          pend_unit = -1;
+        }
+        if (it + 1 < n_it) cur.next(rows_s, per);
+      }
+      if (!ok) {   // copies in flight land before the CTA leaves
+        for (int i = max(0, issued - ST); i < issued; ++i)
+          (void)mbar_wait_bounded(&full_bar[i % ST], (i / ST) & 1);
+        for (int i = max(0, seg - 2); i < seg; ++i) (void)mbar_wait_bounded(&qfull_bar[i & 1], (i >> 1) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 13) {
+    // ================= products =================
+    if (lane == 0) {
+      constexpr uint32_t id_s = tc_idesc(NB, false), id_o = tc_idesc(NB, true);
+      const uint32_t q_addr = smem_u32(q_img), p_addr = smem_u32(p_buf);
+      int seg = -1;
+      bool ok = true, first_prev = false;
+      auto values = [&](int j, bool first) {   // O (+)= V'(j) P(j)
+        if (!(ok = wait(&vfull_bar[0], j & 1) && wait(&pfull_bar[j & 1], (j >> 1) & 1))) return;
+        tc_after();
+        const uint32_t p0 = p_addr + (j & 1) * C::PBUF;
+#pragma unroll
+        for (int k = 0; k < kTreeStep / 16; ++k)
+          tc_mma(tmem + C::OA, tmem + C::VA + 8 * k, tc_desc(p0 + k * 2048), id_o, !first || k > 0);
+        tc_commit(&vempty_bar[0]);
+        if (NRES) {
+          if (!(ok = wait(&vfull_bar[1], j & 1))) return;
+          tc_after();
+#pragma unroll
+          for (int k = 0; k < kTreeStep / 16; ++k)
+            tc_mma(tmem + C::OR, tmem + C::VR + 8 * k, tc_desc(p0 + k * 2048), id_o, !first || k > 0);
+          tc_commit(&vempty_bar[1]);
+        }
+        tc_commit(&pempty_bar[j & 1]);
+      };
+      for (int it = 0; it < n_it && ok; ++it) {
+        const bool first = it == 0 || cur.step == 0;
+        if (first) {
+          ++seg;
+          if (!(ok = wait(&qfull_bar[seg & 1], (seg >> 1) & 1))) break;
+        }
+        const uint32_t q0 = q_addr + (seg & 1) * C::IMG, s0 = tmem + C::S0 + (it % SB) * C::SCOLS;
+        if (!(ok = wait(&sempty_bar[it % SB], ((it / SB) & 1) ^ 1) && wait(&kfull_bar[0], it & 1))) break;
+        tc_after();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma(s0, tmem + C::KA + 8 * k, tc_desc(q0 + (k >> 2) * C::QBLK + (k & 3) * 32), id_s, k > 0);
+        tc_commit(&kempty_bar[0]);
+        if (NRES) {
+          if (!(ok = wait(&kfull_bar[1], it & 1))) break;
+          tc_after();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tc_mma(s0 + NB, tmem + C::KR + 8 * k, tc_desc(q0 + (2 + (k >> 2)) * C::QBLK + (k & 3) * 32), id_s, k > 0);
+          tc_commit(&kempty_bar[1]);
+        }
+        tc_commit(&sfull_bar[it % SB]);
+        if (it + 1 == n_it || cur.step + 1 == cur.steps) tc_commit(&qempty_bar[seg & 1]);
+        if (it > 0) values(it - 1, first_prev);
+        first_prev = first;
+        if (it + 1 < n_it) cur.next(rows_s, per);
+      }
+      if (ok) values(n_it - 1, first_prev);
+      if (!ok) {   // products in flight end before tensor memory is given back
+        tc_commit(&drain_bar);
+        (void)mbar_wait_bounded(&drain_bar, 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ================= K: one token a lane =================
+    const int tok = tid & 63, tau = tid >> 6;
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    for (int it = 0; it < n_it; ++it) {
+      const int st = it % ST;
+      wait_warp(&full_bar[st], (it / ST) & 1);
+      const uint8_t* s = stages + st * C::STAGE;
+      const bool on = tid < valid_of(cur);
+#pragma unroll
+      for (int pl = 0; pl < PL; ++pl) {
+        const uint8_t* tile = pl ? s + C::RK + tau * C::R_TILE : s + tau * C::A_TILE;
+        const uint8_t* row = tile + tok * (pl ? D / 4 : D / 2);
+        const uint8_t* meta = tile + (pl ? C::R_CODES : C::A_CODES) + tok * NG * 2;
+        uint32_t mw[NG / 2];   // two groups a word
+        if (NG == 4) {
+          const uint2 v = *reinterpret_cast<const uint2*>(meta);
+          mw[0] = v.x; mw[1] = v.y;
+        } else if (NG == 8) {
+          const uint4 v = *reinterpret_cast<const uint4*>(meta);
+          mw[0] = v.x; mw[1] = v.y; mw[2 % (NG / 2)] = v.z; mw[3 % (NG / 2)] = v.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < NG / 2; ++i) {
+            const uint16_t* mp = reinterpret_cast<const uint16_t*>(meta) + 2 * i;
+            mw[i] = (uint32_t)mp[0] | (uint32_t)mp[1] << 16;
+          }
+        }
+        auto consts = [&](int gi, __half2* sc, __half2* kc) {
+          uint16_t mb;
+          if (NG & 1)
+            mb = reinterpret_cast<const uint16_t*>(meta)[gi];
+          else
+            mb = (uint16_t)(mw[(gi / 2) % (NG / 2)] >> (16 * (gi & 1)));
+          const __half2 so = e4m3_pair(on ? mb : (uint16_t)0);
+          const __half k = __hfma(__low2half(so), __float2half_rn(pl ? -4.f : -16.f), __high2half(so));
+          *sc = __low2half2(so);
+          *kc = __half2half2(k);
+        };
+        wait_warp(&kempty_bar[pl], (it & 1) ^ 1);
+        tc_after();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {   // 32 channels: 16 columns
+          uint32_t r[16];
+          if (pl == 0) {
+            const uint4 w = reinterpret_cast<const uint4*>(row)[c];
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            __half2 sc, kc;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if ((c * 32 + i * 8) % GS == 0) consts((c * 32 + i * 8) / GS, &sc, &kc);
+              uint32_t v[4];
+              codes4(ww[i], v);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) r[4 * i + j] = h2u(__hfma2(u2h(v[j]), sc, kc));
+            }
+          } else {
+            const uint2 w = reinterpret_cast<const uint2*>(row)[c];
+            const uint32_t ww[2] = {w.x, w.y};
+            __half2 sc, kc;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if ((c * 32 + i * 16) % GS == 0) consts((c * 32 + i * 16) / GS, &sc, &kc);
+              uint32_t v[8];
+              codes2(ww[i], v);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) r[8 * i + j] = h2u(__hfma2(u2h(v[j]), sc, kc));
+            }
+          }
+          tc_st16(lanes + (pl ? C::KR : C::KA) + 16 * c, r);
+        }
+        tc_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kfull_bar[pl]);
+      }
+      if (lane == 0) mbar_arrive(&empty_bar[st]);
+      if (it + 1 < n_it) cur.next(rows_s, per);
+    }
+  } else if (warp < 8) {
+    // ================= softmax: one token a lane =================
+    const int lt = tid - 128, tok = lt & 63, tau = lt >> 6, w4 = warp - 4;
+    const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
+    const int slot = (lt & ~3) + ((lt & 1) << 1 | ((lt >> 1) & 1));   // the token's row of P (the V codes' order)
+    float l[NB];
+    pdl_wait();
+    for (int it = 0; it < n_it; ++it) {
+      const bool first = it == 0 || cur.step == 0;
+      const int unit = cur.b * per + cur.in_row;
+      if (first) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) l[i] = 0.f;
+        if (lt < NB) {
+          qm_s[lt >> 1][lt & 1] = __ldcg(a.q_scale + (size_t)unit * NB + lt);
+          qm_s[lt >> 1][2 + (lt & 1)] = INFINITY;
+        }
+        wg_sync(1);
+      }
+      const int nv = valid_of(cur), st = it % ST;
+      const bool on = lt < nv;
+      float c = 0.f;
+      if (NRES) {
+        wait_warp(&full_bar[st], (it / ST) & 1);
+        const uint16_t cb = *reinterpret_cast<const uint16_t*>(stages + st * C::STAGE + C::RK + tau * C::R_TILE +
+                                                               C::R_CODES + C::META + tok * 2);
+        c = on ? bf16_bits_to_f32(cb) : 0.f;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty_bar[st]);
+      }
+      const float2 c2 = make_float2(c, c);
+      wait_warp(&sfull_bar[it % SB], (it / SB) & 1);
+      tc_after();
+      const uint32_t s0 = lanes + C::S0 + (it % SB) * C::SCOLS;
+      // score products of 16 queries with this lane's token
+      auto scores = [&](int ch, float2 (&y)[8]) {
+        uint32_t ra[16], rr[16];
+        tc_ld16(s0 + 16 * ch, ra);
+        if (NRES) tc_ld16(s0 + NB + 16 * ch, rr);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          y[i] = make_float2(__uint_as_float(ra[2 * i]), __uint_as_float(ra[2 * i + 1]));
+          if (NRES)
+            y[i] = fma2(y[i], c2, make_float2(__uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1])));
+        }
+      };
+      // ... in log2 units, relative to the query's reference
+      auto relative = [&](int ch, float2 (&y)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 k = *reinterpret_cast<const float4*>(qm_s[8 * ch + i]);
+          y[i] = fma2(y[i], make_float2(k.x, k.y), make_float2(k.z, k.w));
+        }
+      };
+      float top = -INFINITY;
+#pragma unroll
+      for (int ch = 0; ch < NB / 16; ++ch) {
+        float2 y[8];
+        scores(ch, y);
+        relative(ch, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(y[i].x, y[i].y));
+      }
+      if (wg_any(1, on && top > kTop)) {
+        // move the references to this step's maxima where those are higher
+#pragma unroll
+        for (int ch = 0; ch < NB / 16; ++ch) {
+          float2 y[8];
+          scores(ch, y);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float v = on ? (i & 1 ? y[i / 2].y : y[i / 2].x) * qm_s[8 * ch + i / 2][i & 1] : -INFINITY;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            if (lane == 0) wred_s[w4][16 * ch + i] = v;
+          }
+        }
+        wg_sync(1);
+        if (lt < NB) {
+          const float old = -qm_s[lt >> 1][2 + (lt & 1)];
+          const float mx = fmaxf(fmaxf(wred_s[0][lt], wred_s[1][lt]), fmaxf(wred_s[2][lt], wred_s[3][lt])) - kHead;
+          const float now = fmaxf(old, mx);
+          f_s[lt] = old == now ? 1.f : exp2f(old - now);
+          qm_s[lt >> 1][2 + (lt & 1)] = -now;
+        }
+        wg_sync(1);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) l[i] *= f_s[i];
+        if (!first) {   // O holds products of the steps before: all of them done, then scaled
+          wait_warp(&pempty_bar[(it - 1) & 1], ((it - 1) >> 1) & 1);
+          tc_after();
+#pragma unroll
+          for (int ch = 0; ch < PL * NB / 16; ++ch) {
+            uint32_t r[16];
+            tc_ld16(lanes + C::OA + 16 * ch, r);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f_s[(16 * ch + i) % NB]);
+            tc_st16(lanes + C::OA + 16 * ch, r);
+          }
+          tc_wait_st();
+        }
+      }
+      // weights
+      wait_warp(&pempty_bar[it & 1], ((it >> 1) & 1) ^ 1);
+      uint8_t* prow = p_buf + (it & 1) * C::PBUF + slot * 128;
+#pragma unroll
+      for (int ch = 0; ch < NB / 16; ++ch) {
+        float2 y[8];
+        scores(ch, y);
+        relative(ch, y);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          y[i].x = on ? ex2_fast(y[i].x) : 0.f;
+          y[i].y = on ? ex2_fast(y[i].y) : 0.f;
+          l[16 * ch + 2 * i] += y[i].x;
+          l[16 * ch + 2 * i + 1] += y[i].y;
+          w[i] = f16x2(y[i].x, y[i].y);
+        }
+        *reinterpret_cast<uint4*>(prow + (((2 * ch) ^ (slot & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(prow + (((2 * ch + 1) ^ (slot & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+      fence_async_smem();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sempty_bar[it % SB]);
+        mbar_arrive(&pfull_bar[it & 1]);
+      }
+      if (it + 1 == n_it || cur.step + 1 == cur.steps) {
+        // the unit's state out
+        wait_warp(&pempty_bar[it & 1], (it >> 1) & 1);
+        tc_after();
+        float* part = a.partials + (size_t)(blockIdx.x + unit) * a.pstride;
+        if (lt < D) {
+#pragma unroll
+          for (int c = 0; c < PL * NB / 16; ++c) {
+            uint32_t r[16];
+            if (D == 128 || w4 < 3) {
+              tc_ld16(lanes + C::OA + 16 * c, r);
+              tc_wait_ld();
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(part + 2 * NB + ((size_t)(4 * c + i) * D + lt) * 4) =
+                  make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+          }
+        }
+        tc_before();
+        // sums over the lanes: reduce-scatter, then over the warps in order
+#pragma unroll
+        for (int o = 16, n = NB / 2; o >= 1; o >>= 1) {
+          if (n >= 1) {
+            const bool up = (lane & o) != 0;
+#pragma unroll
+            for (int i = 0; i < (NB >= 32 ? NB / 2 : 8); ++i)
+              if (i < n) {
+                const float send = up ? l[i] : l[i + n], keep = up ? l[i + n] : l[i];
+                l[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+              }
+            n >>= 1;
+          } else {
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+          }
+        }
+        // NB = 64: lane holds queries q0, q0 + 1 ...: the bits of the lane, highest first
+        if (NB == 64) {
+          wred_s[w4][lane * 2] = l[0];
+          wred_s[w4][lane * 2 + 1] = l[1];
+        } else if (NB == 32) {
+          wred_s[w4][lane] = l[0];
+        } else if ((lane & 1) == 0) {
+          wred_s[w4][lane >> 1] = l[0];
+        }
+        wg_sync(1);
+        if (lt < NB) {
+          part[lt] = -qm_s[lt >> 1][2 + (lt & 1)];
+          part[NB + lt] = wred_s[0][lt] + wred_s[1][lt] + wred_s[2][lt] + wred_s[3][lt];
+        }
+        wg_sync(1);
+      }
+      if (it + 1 < n_it) cur.next(rows_s, per);
+    }
+  } else {
+    // ================= V: one channel a lane =================
+    const int lt = tid - 256, w4 = warp - 8;
+    const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
+    const int col = 2 * (lt >> 2) + (lt & 1), hf = (lt >> 1) & 1;   // the token's place among the constants
+    const int tok = lt & 63, tau = lt >> 6;
+    for (int it = 0; it < n_it; ++it) {
+      const int st = it % ST;
+      wait_warp(&full_bar[st], (it / ST) & 1);
+      const uint8_t* s = stages + st * C::STAGE;
+      const bool on = lt < valid_of(cur);
+      wg_sync(2);   // the previous step's constants are used up
+      // Constants of this lane's token: (f s, f o - 16 f s) for the anchor, (s, o - 4 s) for the
+      // residual.  The coefficient c = m f, f a power of two and 1 <= |m| < 2: powers of two
+      // leave the constants exact, and m multiplies the finished f (s code + o), so that a
+      // value is rounded relative to itself and not to its group's range.
+      float f = 1.f;
+      if (NRES) {
+        const uint16_t cb =
+            *reinterpret_cast<const uint16_t*>(s + C::RV + tau * C::R_TILE + C::R_CODES + C::META + tok * 2);
+        f = __uint_as_float((uint32_t)(cb & 0x7F80) << 16);
+        uint16_t mb = (uint16_t)((cb & 0x807F) | 0x3F80);             // c's sign and significand
+        if ((cb & 0x7F80) == 0) { f = 1.f; mb = 0; }                  // zero (a subnormal c counts as zero)
+        if ((cb & 0x7F80) == 0x7F80) { f = 1.f; mb = cb; }            // infinite, NaN: stays
+        *reinterpret_cast<__half*>(tab + PL * NG * 512 + col * 4 + hf * 2) =
+            __float2half_rn(on ? bf16_bits_to_f32(mb) : 0.f);
+      }
+#pragma unroll
+      for (int pl = 0; pl < PL; ++pl) {
+        const uint8_t* tile = pl ? s + C::RV + tau * C::R_TILE : s + C::AV + tau * C::A_TILE;
+        const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + (pl ? C::R_CODES : C::A_CODES)) + tok * NG;
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+          const float2 so = e4m3x2_to_f32x2(meta[gi]);
+          const float g = pl ? 1.f : f;
+          __half sh = half_sat(so.x * g);
+          __half kh = half_sat(fmaf(pl ? -4.f : -16.f, __half2float(sh), so.y * g));
+          if (!on) sh = kh = __ushort_as_half(0);
+          uint8_t* e = tab + ((pl * NG + gi) * 64 + col) * 8 + hf * 2;
+          *reinterpret_cast<__half*>(e) = sh;
+          *reinterpret_cast<__half*>(e + 4) = kh;
+        }
+      }
+      wg_sync(2);
+#pragma unroll
+      for (int pl = 0; pl < PL; ++pl) {
+        wait_warp(&vempty_bar[pl], (it & 1) ^ 1);
+        tc_after();
+        if (D == 128 || w4 < 3) {
+          const uint8_t* tile = pl ? s + C::RV : s + C::AV;
+          const uint4* tb = reinterpret_cast<const uint4*>(tab + (pl * NG + lt / GS) * 64 * 8);
+          const uint4* cm = reinterpret_cast<const uint4*>(tab + PL * NG * 512);   // significands of c
+#pragma unroll
+          for (int c4 = 0; c4 < 4; ++c4) {   // 32 tokens: 16 columns
+            uint32_t r[16];
+            const uint8_t* row = tile + (c4 >> 1) * (pl ? C::R_TILE : C::A_TILE) + lt * (pl ? 16 : 32);
+            if (pl == 0) {
+              const uint4 w = reinterpret_cast<const uint4*>(row)[c4 & 1];
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {    // word: tokens 8 i ..; columns 4 i ..
+                uint32_t v[4];
+                codes4(ww[i], v);
+                // masks leave tokens (0, 2), (4, 6), (1, 3), (5, 7); columns hold (0, 2), (1, 3), (4, 6), (5, 7)
+                const uint4 k0 = tb[c4 * 8 + 2 * i], k1 = tb[c4 * 8 + 2 * i + 1];
+                r[4 * i] = h2u(__hfma2(u2h(v[0]), u2h(k0.x), u2h(k0.y)));
+                r[4 * i + 1] = h2u(__hfma2(u2h(v[2]), u2h(k0.z), u2h(k0.w)));
+                r[4 * i + 2] = h2u(__hfma2(u2h(v[1]), u2h(k1.x), u2h(k1.y)));
+                r[4 * i + 3] = h2u(__hfma2(u2h(v[3]), u2h(k1.z), u2h(k1.w)));
+                if (NRES) {
+                  const uint4 m = cm[c4 * 4 + i];
+                  r[4 * i] = h2u(__hmul2(u2h(r[4 * i]), u2h(m.x)));
+                  r[4 * i + 1] = h2u(__hmul2(u2h(r[4 * i + 1]), u2h(m.y)));
+                  r[4 * i + 2] = h2u(__hmul2(u2h(r[4 * i + 2]), u2h(m.z)));
+                  r[4 * i + 3] = h2u(__hmul2(u2h(r[4 * i + 3]), u2h(m.w)));
+                }
+              }
+            } else {
+              const uint2 w = reinterpret_cast<const uint2*>(row)[c4 & 1];
+              const uint32_t ww[2] = {w.x, w.y};
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {    // word: tokens 16 i ..; columns 8 i ..
+                uint32_t v[8];
+                codes2(ww[i], v);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {  // quad m: columns (0, 2), (1, 3)
+                  const uint4 k0 = tb[c4 * 8 + 4 * i + m];
+                  r[8 * i + 2 * m] = h2u(__hfma2(u2h(v[m]), u2h(k0.x), u2h(k0.y)));
+                  r[8 * i + 2 * m + 1] = h2u(__hfma2(u2h(v[4 + m]), u2h(k0.z), u2h(k0.w)));
+                }
+              }
+            }
+            tc_st16(lanes + (pl ? C::VR : C::VA) + 16 * c4, r);
+          }
+          tc_wait_st();
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&vfull_bar[pl]);
+      }
+      if (lane == 0) mbar_arrive(&empty_bar[st]);
+      if (it + 1 < n_it) cur.next(rows_s, per);
+    }
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_after();
+    tc_dealloc(tmem, 512);
+  }
+}
+
+// ---- merge -------------------------------------------------------------------------
+// One CTA per kMergeQ queries of a (row, KV head), thread = channel.  The drafted tokens
+// first (BF16 keys and values, float32 arithmetic; before the wait: nothing of it
+// depends on the streaming kernel), then the partial states, R^T, the quotient.
+template <int D, int NRES, int NB>
+__global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, int ctas) {
+  __shared__ TreeRowsShared rows_s;
+  __shared__ __align__(16) float q_s[128][kMergeQ];          // [channel][query]
+  __shared__ __align__(16) float p_s[128][kMergeQ];          // [key][query], then R^T's operand [channel][query]
+  __shared__ unsigned long long vis_s[kMergeQ][RQ_MAX_TREE_NODES / 64];
+  __shared__ float red_s[4][kMergeQ];
+  __shared__ int range_s[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per_bh = (a.M + kMergeQ - 1) / kMergeQ;
+  const int bh = blockIdx.x / per_bh, r0 = blockIdx.x % per_bh * kMergeQ, b = bh / a.g.H;
+  const int nq = min(kMergeQ, a.M - r0);
+  tree_rows(a, &rows_s);
+  const int cnt = a.counts ? clamp_len(a.counts[b], a.T) : a.T;
+  const __nv_bfloat16* qp = a.q + ((size_t)bh * a.M + r0) * D;
+  for (int i = tid; i < kMergeQ * D; i += 128) {
+    const int qi = i / D, ch = i % D;
+    q_s[ch][qi] = qi < nq ? __bfloat162float(qp[(size_t)qi * D + ch]) : 0.f;
+  }
+  if (tid < kMergeQ * (RQ_MAX_TREE_NODES / 64)) {
+    const int qi = tid % kMergeQ, w = tid / kMergeQ, t = (r0 + qi) % a.T;
+    unsigned long long v = 0;
+    if (qi < nq && t < cnt && w * 64 < cnt) {
+      v = a.mask ? __ldg(a.mask + ((size_t)b * a.T + t) * a.words + w)
+                 : (t >= w * 64 + 63 ? ~0ull : (t < w * 64 ? 0ull : (2ull << (t - w * 64)) - 1ull));
+      if (cnt - w * 64 < 64) v &= (1ull << (cnt - w * 64)) - 1ull;
+    }
+    vis_s[qi][w] = v;
+  }
+  __syncthreads();
+
+  float m[kMergeQ], l[kMergeQ], o[kMergeQ];
+#pragma unroll
+  for (int i = 0; i < kMergeQ; ++i) { m[i] = -INFINITY; l[i] = 0.f; o[i] = 0.f; }
+  const __nv_bfloat16* kp = a.k_new + (size_t)bh * a.T * D;
+  const __nv_bfloat16* vp = a.v_new + (size_t)bh * a.T * D;
+  for (int j0 = 0; j0 < cnt; j0 += 128) {
+    const int j = j0 + tid;
+    float s[kMergeQ];
+#pragma unroll
+    for (int i = 0; i < kMergeQ; ++i) s[i] = 0.f;
+    if (j < cnt) {
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(kp + (size_t)j * D) + c);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float k = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+#pragma unroll
+          for (int i = 0; i < kMergeQ; ++i) s[i] = fmaf(k, q_s[8 * c + e][i], s[i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeQ; ++i) {
+      const bool on = j < cnt && ((vis_s[i][j >> 6] >> (j & 63)) & 1);
+      s[i] = on ? s[i] * a.qscale : -INFINITY;
+      float v = s[i];
+#pragma unroll
+      for (int f = 16; f > 0; f >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, f));
+      if (lane == 0) red_s[warp][i] = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMergeQ; ++i) {
+      const float now = fmaxf(m[i], fmaxf(fmaxf(red_s[0][i], red_s[1][i]), fmaxf(red_s[2][i], red_s[3][i])));
+      const float ref = now == -INFINITY ? 0.f : now;
+      const float f = exp2f(m[i] - ref);
+      l[i] *= f;
+      o[i] *= f;
+      m[i] = now;
+      const bool on = j < cnt && ((vis_s[i][j >> 6] >> (j & 63)) & 1);
+      s[i] = on ? exp2f(s[i] - ref) : 0.f;
+      p_s[tid][i] = s[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMergeQ; ++i) {
+      float v = s[i];
+#pragma unroll
+      for (int f = 16; f > 0; f >>= 1) v += __shfl_xor_sync(0xffffffffu, v, f);
+      if (lane == 0) red_s[warp][i] = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMergeQ; ++i) l[i] += (red_s[0][i] + red_s[1][i]) + (red_s[2][i] + red_s[3][i]);
+    if (tid < D) {
+      const int nk = min(128, cnt - j0);
+      for (int k = 0; k < nk; ++k) {
+        const float v = __bfloat162float(vp[(size_t)(j0 + k) * D + tid]);
+        if (isfinite(v)) {
+#pragma unroll
+          for (int i = 0; i < kMergeQ; ++i) o[i] = fmaf(p_s[k][i], v, o[i]);
+        } else {   // enters only where it is seen
+#pragma unroll
+          for (int i = 0; i < kMergeQ; ++i)
+            if ((vis_s[i][(j0 + k) >> 6] >> ((j0 + k) & 63)) & 1) o[i] = fmaf(p_s[k][i], v, o[i]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+
+  // the cached tokens' partial states
+  if (tid == 0) {
+    const int U = rows_s.pre[a.batch];
+    const int steps = (rows_s.len[b] + kTreeStep - 1) / kTreeStep;
+    range_s[0] = 0;
+    range_s[1] = -1;
+    if (steps) {
+      const TreeSplit split{U / ctas, U % ctas};
+      const int unit = bh * a.nqb + r0 / NB;
+      const int s0 = rows_s.pre[b] + (unit - b * a.g.H * a.nqb) * steps;
+      range_s[0] = split.owner(s0);
+      range_s[1] = split.owner(s0 + steps - 1);
+    }
+  }
+  pdl_wait();
+  __syncthreads();
+  const int c_lo = range_s[0], c_hi = range_s[1];
+  const int unit = bh * a.nqb + r0 / NB, qo = r0 % NB;
+  const float* part = a.partials + (size_t)unit * a.pstride;
+  // common reference
+  float mine[kMergeQ];
+#pragma unroll
+  for (int i = 0; i < kMergeQ; ++i) mine[i] = m[i];
+  for (int c = c_lo; c <= c_hi; ++c) {
+#pragma unroll
+    for (int i = 0; i < kMergeQ; ++i) mine[i] = fmaxf(mine[i], __ldcg(part + (size_t)c * a.pstride + qo + i));
+  }
+  float orr[kMergeQ];
+#pragma unroll
+  for (int i = 0; i < kMergeQ; ++i) {
+    if (mine[i] == -INFINITY) mine[i] = 0.f;
+    const float f = exp2f(m[i] - mine[i]);
+    l[i] *= f;
+    o[i] *= f;
+    orr[i] = 0.f;
+  }
+  for (int c = c_lo; c <= c_hi; ++c) {
+    const float* p = part + (size_t)c * a.pstride;
+    float f[kMergeQ];
+#pragma unroll
+    for (int i = 0; i < kMergeQ; ++i) {
+      f[i] = exp2f(__ldcg(p + qo + i) - mine[i]);
+      l[i] = fmaf(f[i], __ldcg(p + NB + qo + i), l[i]);
+    }
+    if (tid < D) {
+#pragma unroll
+      for (int i4 = 0; i4 < kMergeQ / 4; ++i4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + 2 * NB) + (size_t)(qo / 4 + i4) * D + tid);
+        o[4 * i4] = fmaf(f[4 * i4], x.x, o[4 * i4]);
+        o[4 * i4 + 1] = fmaf(f[4 * i4 + 1], x.y, o[4 * i4 + 1]);
+        o[4 * i4 + 2] = fmaf(f[4 * i4 + 2], x.z, o[4 * i4 + 2]);
+        o[4 * i4 + 3] = fmaf(f[4 * i4 + 3], x.w, o[4 * i4 + 3]);
+        if (NRES) {
+          const float4 y =
+              __ldcg(reinterpret_cast<const float4*>(p + 2 * NB) + (size_t)(NB / 4 + qo / 4 + i4) * D + tid);
+          orr[4 * i4] = fmaf(f[4 * i4], y.x, orr[4 * i4]);
+          orr[4 * i4 + 1] = fmaf(f[4 * i4 + 1], y.y, orr[4 * i4 + 1]);
+          orr[4 * i4 + 2] = fmaf(f[4 * i4 + 2], y.z, orr[4 * i4 + 2]);
+          orr[4 * i4 + 3] = fmaf(f[4 * i4 + 3], y.w, orr[4 * i4 + 3]);
+        }
+      }
+    }
+  }
+  if (NRES && c_hi >= c_lo) {   // R^T: thread = output channel
+    if ((a.g.mode & RQ_MODE_HADAMARD) != 0) {
+      hadamard128<kMergeQ>(orr, tid, &q_s[0][0]);
+#pragma unroll
+      for (int i = 0; i < kMergeQ; ++i) o[i] += orr[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kMergeQ; ++i) p_s[tid][i] = orr[i];
+      __syncthreads();
+      if (tid < D) {
+#pragma unroll 8
+        for (int k = 0; k < D; ++k) {
+          const float r = __ldg(a.R + (size_t)k * D + tid);
+          const float4 x = *reinterpret_cast<const float4*>(p_s[k]), y = *reinterpret_cast<const float4*>(p_s[k] + 4);
+          o[0] = fmaf(r, x.x, o[0]); o[1] = fmaf(r, x.y, o[1]); o[2] = fmaf(r, x.z, o[2]); o[3] = fmaf(r, x.w, o[3]);
+          o[4] = fmaf(r, y.x, o[4]); o[5] = fmaf(r, y.y, o[5]); o[6] = fmaf(r, y.z, o[6]); o[7] = fmaf(r, y.w, o[7]);
+        }
+      }
+    }
+  }
+  if (tid < D) {
+    __nv_bfloat16* op = a.out + ((size_t)bh * a.M + r0) * D + tid;
+#pragma unroll
+    for (int i = 0; i < kMergeQ; ++i)
+      if (i < nq && (r0 + i) % a.T < cnt)
+        op[(size_t)i * D] = __float2bfloat16_rn(l[i] != 0.f ? o[i] / l[i] : 0.f);   // no key seen: zero; NaN stays
+  }
+}
+
+template <int D, int GS, int NRES, int NB>
+cudaError_t launch_tree_t(const TreeArgs& args, int num_sms, cudaStream_t stream) {
+  using C = TreeCfg<D, GS, NRES, NB>;
+  TreeArgs a = args;
+  a.pstride = C::PSTRIDE;
+  auto* kern = tree_mma_kernel<D, GS, NRES, NB>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int units = a.batch * a.g.H * a.nqb;
+  e = launch_dependent(tree_prep_kernel<D, NRES, NB>, dim3(units * (NB / kPrepQ)), dim3(256), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kern, dim3(num_sms), dim3(kTreeThreads), (size_t)C::SMEM, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(tree_merge_kernel<D, NRES, NB>, dim3(a.batch * a.g.H * ((a.M + kMergeQ - 1) / kMergeQ)),
+                          dim3(128), 0, stream, a, num_sms);
+}
+
+template <int D, int GS, int NRES>
+cudaError_t launch_tree_nb(const TreeArgs& a, int nb, int num_sms, cudaStream_t stream) {
+  if (nb == 16) return launch_tree_t<D, GS, NRES, 16>(a, num_sms, stream);
+  if (nb == 32) return launch_tree_t<D, GS, NRES, 32>(a, num_sms, stream);
+  return launch_tree_t<D, GS, NRES, 64>(a, num_sms, stream);
+}
+
+template <int D>
+cudaError_t launch_tree_d(const TreeArgs& a, int nb, int num_sms, cudaStream_t stream) {
+  if (a.g.g == 32)
+    return a.nres ? launch_tree_nb<D, 32, 1>(a, nb, num_sms, stream) : launch_tree_nb<D, 32, 0>(a, nb, num_sms, stream);
+  return a.nres ? launch_tree_nb<D, 16, 1>(a, nb, num_sms, stream) : launch_tree_nb<D, 16, 0>(a, nb, num_sms, stream);
+}
+
+}  // namespace
+}  // namespace rq

@@ -1,10 +1,14 @@
 """GPU: attention of drafted tokens (rq_tree_attention) against float64.
 
-Bar: |gpu - float64| <= 2e-3 + 2^-8 |float64|: the library's bar for decode
-attention on O(1) data plus half a BF16 step for the rounded result.  Queries,
-rebuilt K/V and weights carry 11 significant bits in the kernel: a score of
-O(10) standard size then moves by about 2^-11 of sqrt(d) |q k| scale, some 3e-4,
-and the result by as much of its spread, which the 2e-3 covers.
+Bar: |gpu - float64| <= 2e-3 + 2^-8 |float64| + 2 * 2^-11 sum p |v|: the library's
+bar for decode attention on O(1) data, half a BF16 step for the rounded result, and
+the half steps of 11-bit operands in the value sum.  That sum is of products p v, with
+p and v (the anchor's part c a of it) each rounded to 11 significant bits, half a step
+or 2^-11 of the value: a product is off by at most 2 * 2^-11 of p |v| to first order.
+Where channels are outliers (values of 8 to 30), few keys share the weight and the values
+cancel, that exceeds 2e-3.  The residual's part R^T r, at most about 1, separates c a from
+v by 2^-10, inside the 2e-3; queries are BF16 and so exact in 11 bits, only R q rounds:
+a score moves by some 2^-11 |R q| |r| scale, 2e-4 at most.
 """
 import math
 
@@ -18,7 +22,7 @@ from test_gpu_paged import PagedCache, _table
 
 pytestmark = pytest.mark.gpu
 
-ATOL, RTOL = 2e-3, 2.0 ** -8
+ATOL, RTOL, VTOL = 2e-3, 2.0 ** -8, 2 * 2.0 ** -11
 FILL = 7.0          # what output rows hold before the call
 
 
@@ -52,10 +56,20 @@ def bf16(rng, *shape):
     return t, t.double().numpy()
 
 
+class Ref:
+    """Float64 results and, per element, sum p |v|."""
+
+    def __init__(self, out, size):
+        self.out, self.size = out, size
+
+    def __getitem__(self, at):
+        return Ref(self.out[at], self.size[at])
+
+
 def reference(obuf, geom, R, case, layer, group, loop, q, kn, vn, see, counts, lens, scale):
     B, Hq, T, d = q.shape
     qpk = Hq // case.H
-    out = np.full(q.shape, FILL)
+    out, size = np.full(q.shape, FILL), np.zeros(q.shape)
     for b in range(B):
         n, m = int(lens[b]), int(counts[b])
         for h in range(case.H):
@@ -72,7 +86,8 @@ def reference(obuf, geom, R, case, layer, group, loop, q, kn, vn, see, counts, l
                     with np.errstate(invalid="ignore"):
                         p = np.exp(s - s.max())
                         out[b, hq, t] = (p / p.sum()) @ vals
-    return out
+                        size[b, hq, t] = (p / p.sum()) @ np.abs(vals)
+    return Ref(out, size)
 
 
 def call(gpu, layer, group, loop, q, kn, vn, mask, counts, lens, scale, out=None, ws=None):
@@ -112,7 +127,7 @@ def filled(case, seed, ntok, paged=False, layer=0, group=0):
 
 def check(out, ref, what):
     got = out.double().cpu().numpy()
-    err = np.abs(got - ref) - RTOL * np.abs(ref)
+    err = np.abs(got - ref.out) - RTOL * np.abs(ref.out) - VTOL * ref.size
     worst = float(err.max())
     assert worst <= ATOL, f"{what}: {worst:.3e} beyond half a BF16 step"
     return worst
@@ -171,7 +186,10 @@ def test_single_token_agrees_with_the_decode_call_and_null_mask_is_a_sequence():
         vb, _ = bf16(rng, 3, 4, 1, 128)
         one = gpu.decode(0, 0, loop, qb[:, :, 0], kb[:, :, 0], vb[:, :, 0], lens, scale)
         out = call(gpu, 0, 0, loop, qb, kb, vb, None, None, lens, scale)
-        check(out[:, :, 0], one.double().cpu().numpy(), f"loop {loop}")
+        ref = reference(obuf, geom, R, case, 0, 0, loop, qb.double().numpy(), kb.double().numpy(),
+                        vb.double().numpy(), np.ones((3, 1, 1), dtype=bool), [1] * 3, lens, scale)
+        check(out, ref, f"loop {loop}")
+        check(out, Ref(one.double().cpu().numpy()[:, :, None], ref.size), f"loop {loop}, decode call")
     T = 70
     qb, q = bf16(rng, 3, 4, T, 128)
     kb, kn = bf16(rng, 3, 4, T, 128)
@@ -231,7 +249,8 @@ def test_peaky_and_flat_softmax(gain):
     # over 1000 keys; a weight moves by as much, the result by that times the spread of V (about 9)
     move = 6 * 2.0 ** -11 * scale * math.sqrt(2) * np.sqrt((qb.double().numpy()[0, 0][:, None] ** 2 * K[None] ** 2).sum(-1)).max()
     tol = max(ATOL, 9 * move)
-    assert (np.abs(got - ref) <= tol + RTOL * np.abs(ref)).all(), np.abs(got - ref).max()
+    off = np.abs(got - ref.out)
+    assert (off <= tol + RTOL * np.abs(ref.out) + VTOL * ref.size).all(), off.max()
     gpu.close()
 
 
