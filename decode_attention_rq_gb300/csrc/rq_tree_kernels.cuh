@@ -101,12 +101,21 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
                : "memory");
 }
 // D[128 x N] (+)= A[128 x 16] B[16 x N]: A in tensor memory, B in shared memory
-__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+template <bool ACC>
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "r"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
       : "memory");
+}
+// One lane of a converged warp.  The compiler then knows that a single thread issues what
+// follows and keeps the operands in uniform registers: 12 to 16 clocks a product of 16
+// columns, against 50 behind a test of the lane number.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -151,6 +160,21 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// The wait behind a failed first try: until the phase ends, or the CTA gives up (out of
+// line: it is used in some thirty places, and instruction fetch bounds the streaming kernel)
+__device__ __noinline__ bool tree_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                            int32_t* status) {
+  const unsigned long long t0 = global_ns();
+  while (!*abort_flag) {
+    if (mbar_try_wait_sleep(bar, parity)) return true;
+    if (global_ns() - t0 > kWaitNs) {
+      *abort_flag = 1;
+      atomicExch(&status[0], 1);
+    }
+  }
+  return false;
+}
+
 // ---- f16 pairs ---------------------------------------------------------------------
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
@@ -158,11 +182,6 @@ __device__ __forceinline__ __half2 e4m3_pair(uint16_t v) {   // (scale, offset),
   uint32_t h2;
   asm("{\n\t.reg .b16 t;\n\tmov.b16 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h2) : "h"(v));
   return u2h(h2);
-}
-__device__ __forceinline__ __half half_sat(float x) {
-  uint32_t r;
-  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.f), "f"(x));
-  return __low2half(u2h(r));
 }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -405,7 +424,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
   uint8_t* stages = p_buf + 2 * C::PBUF;
   uint8_t* tab = stages + ST * C::STAGE;
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int per = a.g.H * a.nqb;
 
   tree_rows(a, &rows_s);
@@ -445,16 +464,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
   // and let what they issued finish; the other roles run on to their end without
   // waiting (their warps share named barriers, so none may leave alone).
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
-    while (!abort_s) {
-      if (mbar_try_wait_sleep(bar, parity)) return true;
-      if (global_ns() - t0 > kWaitNs) {
-        abort_s = 1;
-        atomicExch(&a.status[0], 1);
-      }
-    }
-    return false;
+    return mbar_try_wait(bar, parity) || tree_wait_long(bar, parity, &abort_s, a.status);
   };
   // the same by a whole warp, which goes on together (the tcgen05 loads and stores are warp-wide)
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
@@ -489,6 +499,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         uint8_t* dst = stages + st * C::STAGE;
         mbar_arrive_expect_tx(&full_bar[st], tiles * (2 * C::A_TILE + NRES * 2 * C::R_TILE));
         if (!a.g.paged) {      // the two tiles of a plane are neighbours
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
             bulk_g2s_hint(dst + kv * C::AV, a.base + a.g.tile_offset(a.layer, a.group, cur.b, h, true, 0, kv, t0, 0),
                           tiles * C::A_TILE, &full_bar[st], pol);
@@ -498,9 +509,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
                             tiles * C::R_TILE, &full_bar[st], pol);
           }
         } else {
+#pragma unroll 1
           for (int i = 0; i < tiles; ++i) {
             int page = checked_page(a.g, raw_page(a.g, cur.b, t0 + i), a.status);
             if (page < 0) page = 0;
+#pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
               bulk_g2s_hint(dst + kv * C::AV + i * C::A_TILE,
                             a.base + a.g.tile_offset(a.layer, a.group, cur.b, h, true, 0, kv, t0 + i, page), C::A_TILE,
@@ -538,61 +551,65 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     __syncwarp();
   } else if (warp == 13) {
     // ================= products =================
-    if (lane == 0) {
-      constexpr uint32_t id_s = tc_idesc(NB, false), id_o = tc_idesc(NB, true);
-      const uint32_t q_addr = smem_u32(q_img), p_addr = smem_u32(p_buf);
-      int seg = -1;
-      bool ok = true, first_prev = false;
-      auto values = [&](int j, bool first) {   // O (+)= V'(j) P(j)
-        if (!(ok = wait(&vfull_bar[0], j & 1) && wait(&pfull_bar[j & 1], (j >> 1) & 1))) return;
+    constexpr uint32_t id_s = tc_idesc(NB, false), id_o = tc_idesc(NB, true);
+    const uint64_t q_desc = tc_desc(smem_u32(q_img)), p_desc = tc_desc(smem_u32(p_buf));
+    int seg = -1;
+    bool ok = true, first_prev = false;
+    // O (+)= V'(j) P(j)
+    auto values = [&](int j, bool first) {
+      const uint64_t p0 = p_desc + (j & 1) * (C::PBUF >> 4);
+#pragma unroll
+      for (int pl = 0; pl < PL; ++pl) {
+        if (!(ok = ok && wait(&vfull_bar[pl], j & 1) && (pl || wait(&pfull_bar[j & 1], (j >> 1) & 1)))) return;
         tc_after();
-        const uint32_t p0 = p_addr + (j & 1) * C::PBUF;
+        __syncwarp();
+        const uint32_t o = tmem + (pl ? C::OR : C::OA), v = tmem + (pl ? C::VR : C::VA);
+        if (elect_one()) {
+          if (first) tc_mma<false>(o, v, p0, id_o); else tc_mma<true>(o, v, p0, id_o);
 #pragma unroll
-        for (int k = 0; k < kTreeStep / 16; ++k)
-          tc_mma(tmem + C::OA, tmem + C::VA + 8 * k, tc_desc(p0 + k * 2048), id_o, !first || k > 0);
-        tc_commit(&vempty_bar[0]);
-        if (NRES) {
-          if (!(ok = wait(&vfull_bar[1], j & 1))) return;
-          tc_after();
+          for (int k = 1; k < kTreeStep / 16; ++k) tc_mma<true>(o, v + 8 * k, p0 + k * (2048 >> 4), id_o);
+          tc_commit(&vempty_bar[pl]);
+          if (pl == PL - 1) tc_commit(&pempty_bar[j & 1]);
+        }
+        __syncwarp();
+      }
+    };
+    for (int it = 0; it < n_it; ++it) {
+      const bool first = it == 0 || cur.step == 0;
+      if (first) {
+        ++seg;
+        ok = ok && wait(&qfull_bar[seg & 1], (seg >> 1) & 1);
+      }
+      const uint64_t q0 = q_desc + (seg & 1) * (C::IMG >> 4);
+      ok = ok && wait(&sempty_bar[it % SB], ((it / SB) & 1) ^ 1);
 #pragma unroll
-          for (int k = 0; k < kTreeStep / 16; ++k)
-            tc_mma(tmem + C::OR, tmem + C::VR + 8 * k, tc_desc(p0 + k * 2048), id_o, !first || k > 0);
-          tc_commit(&vempty_bar[1]);
-        }
-        tc_commit(&pempty_bar[j & 1]);
-      };
-      for (int it = 0; it < n_it && ok; ++it) {
-        const bool first = it == 0 || cur.step == 0;
-        if (first) {
-          ++seg;
-          if (!(ok = wait(&qfull_bar[seg & 1], (seg >> 1) & 1))) break;
-        }
-        const uint32_t q0 = q_addr + (seg & 1) * C::IMG, s0 = tmem + C::S0 + (it % SB) * C::SCOLS;
-        if (!(ok = wait(&sempty_bar[it % SB], ((it / SB) & 1) ^ 1) && wait(&kfull_bar[0], it & 1))) break;
+      for (int pl = 0; pl < PL; ++pl) {
+        if (!(ok = ok && wait(&kfull_bar[pl], it & 1))) break;
         tc_after();
+        __syncwarp();
+        const uint32_t d = tmem + C::S0 + (it % SB) * C::SCOLS + pl * NB, k0 = tmem + (pl ? C::KR : C::KA);
+        if (elect_one()) {
+          tc_mma<false>(d, k0, q0 + pl * (2 * C::QBLK >> 4), id_s);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc_mma(s0, tmem + C::KA + 8 * k, tc_desc(q0 + (k >> 2) * C::QBLK + (k & 3) * 32), id_s, k > 0);
-        tc_commit(&kempty_bar[0]);
-        if (NRES) {
-          if (!(ok = wait(&kfull_bar[1], it & 1))) break;
-          tc_after();
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc_mma(s0 + NB, tmem + C::KR + 8 * k, tc_desc(q0 + (2 + (k >> 2)) * C::QBLK + (k & 3) * 32), id_s, k > 0);
-          tc_commit(&kempty_bar[1]);
+          for (int k = 1; k < D / 16; ++k)
+            tc_mma<true>(d, k0 + 8 * k, q0 + ((pl * 2 + (k >> 2)) * C::QBLK >> 4) + (k & 3) * 2, id_s);
+          tc_commit(&kempty_bar[pl]);
+          if (pl == PL - 1) {
+            tc_commit(&sfull_bar[it % SB]);
+            if (it + 1 == n_it || cur.step + 1 == cur.steps) tc_commit(&qempty_bar[seg & 1]);
+          }
         }
-        tc_commit(&sfull_bar[it % SB]);
-        if (it + 1 == n_it || cur.step + 1 == cur.steps) tc_commit(&qempty_bar[seg & 1]);
-        if (it > 0) values(it - 1, first_prev);
-        first_prev = first;
-        if (it + 1 < n_it) cur.next(rows_s, per);
+        __syncwarp();
       }
-      if (ok) values(n_it - 1, first_prev);
-      if (!ok) {   // products in flight end before tensor memory is given back
-        tc_commit(&drain_bar);
-        (void)mbar_wait_bounded(&drain_bar, 0);
-      }
+      if (ok && it > 0) values(it - 1, first_prev);
+      if (!ok) break;
+      first_prev = first;
+      if (it + 1 < n_it) cur.next(rows_s, per);
+    }
+    if (ok) values(n_it - 1, first_prev);
+    if (__any_sync(0xffffffffu, !ok)) {   // products in flight end before tensor memory is given back
+      if (elect_one()) tc_commit(&drain_bar);
+      (void)mbar_wait_bounded(&drain_bar, 0);
     }
     __syncwarp();
   } else if (warp < 4) {
@@ -608,35 +625,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       for (int pl = 0; pl < PL; ++pl) {
         const uint8_t* tile = pl ? s + C::RK + tau * C::R_TILE : s + tau * C::A_TILE;
         const uint8_t* row = tile + tok * (pl ? D / 4 : D / 2);
-        const uint8_t* meta = tile + (pl ? C::R_CODES : C::A_CODES) + tok * NG * 2;
-        uint32_t mw[NG / 2];   // two groups a word
-        if (NG == 4) {
-          const uint2 v = *reinterpret_cast<const uint2*>(meta);
-          mw[0] = v.x; mw[1] = v.y;
-        } else if (NG == 8) {
-          const uint4 v = *reinterpret_cast<const uint4*>(meta);
-          mw[0] = v.x; mw[1] = v.y; mw[2 % (NG / 2)] = v.z; mw[3 % (NG / 2)] = v.w;
-        } else {
-#pragma unroll
-          for (int i = 0; i < NG / 2; ++i) {
-            const uint16_t* mp = reinterpret_cast<const uint16_t*>(meta) + 2 * i;
-            mw[i] = (uint32_t)mp[0] | (uint32_t)mp[1] << 16;
-          }
-        }
+        const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + (pl ? C::R_CODES : C::A_CODES)) + tok * NG;
+        // (s, s) and (o - 16 s or o - 4 s, twice) of group gi
         auto consts = [&](int gi, __half2* sc, __half2* kc) {
-          uint16_t mb;
-          if (NG & 1)
-            mb = reinterpret_cast<const uint16_t*>(meta)[gi];
-          else
-            mb = (uint16_t)(mw[(gi / 2) % (NG / 2)] >> (16 * (gi & 1)));
-          const __half2 so = e4m3_pair(on ? mb : (uint16_t)0);
-          const __half k = __hfma(__low2half(so), __float2half_rn(pl ? -4.f : -16.f), __high2half(so));
+          const __half2 so = e4m3_pair(on ? meta[gi] : (uint16_t)0);
           *sc = __low2half2(so);
-          *kc = __half2half2(k);
+          *kc = __half2half2(__hfma(__low2half(so), __float2half_rn(pl ? -4.f : -16.f), __high2half(so)));
         };
         wait_warp(&kempty_bar[pl], (it & 1) ^ 1);
         tc_after();
-#pragma unroll
+#pragma unroll 1   // straight-line code for every chunk would stream through the instruction caches
         for (int c = 0; c < D / 32; ++c) {   // 32 channels: 16 columns
           uint32_t r[16];
           if (pl == 0) {
@@ -645,7 +643,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
             __half2 sc, kc;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if ((c * 32 + i * 8) % GS == 0) consts((c * 32 + i * 8) / GS, &sc, &kc);
+              if (i * 8 % GS == 0) consts(c * (32 / GS) + i * 8 / GS, &sc, &kc);
               uint32_t v[4];
               codes4(ww[i], v);
 #pragma unroll
@@ -657,7 +655,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
             __half2 sc, kc;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              if ((c * 32 + i * 16) % GS == 0) consts((c * 32 + i * 16) / GS, &sc, &kc);
+              if (i * 16 % GS == 0) consts(c * (32 / GS) + i * 16 / GS, &sc, &kc);
               uint32_t v[8];
               codes2(ww[i], v);
 #pragma unroll
@@ -875,16 +873,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       // residual.  The coefficient c = m f, f a power of two and 1 <= |m| < 2: powers of two
       // leave the constants exact, and m multiplies the finished f (s code + o), so that a
       // value is rounded relative to itself and not to its group's range.
-      float f = 1.f;
+      __half2 f1 = __half2half2(__ushort_as_half(0x3C00)), f2 = f1;
       if (NRES) {
-        const uint16_t cb =
+        uint16_t cb =
             *reinterpret_cast<const uint16_t*>(s + C::RV + tau * C::R_TILE + C::R_CODES + C::META + tok * 2);
-        f = __uint_as_float((uint32_t)(cb & 0x7F80) << 16);
-        uint16_t mb = (uint16_t)((cb & 0x807F) | 0x3F80);             // c's sign and significand
-        if ((cb & 0x7F80) == 0) { f = 1.f; mb = 0; }                  // zero (a subnormal c counts as zero)
-        if ((cb & 0x7F80) == 0x7F80) { f = 1.f; mb = cb; }            // infinite, NaN: stays
-        *reinterpret_cast<__half*>(tab + PL * NG * 512 + col * 4 + hf * 2) =
-            __float2half_rn(on ? bf16_bits_to_f32(mb) : 0.f);
+        if ((cb & 0x7F80) == 0 || !on) cb = 0;                          // a subnormal c counts as zero
+        const int e = (cb >> 7) & 0xFF;
+        // f = 2^(e - 127) as two factors of f16 range; infinite and NaN c keep f = 1
+        const int x = e == 0 || e == 255 ? 0 : e - 127, x1 = min(max(x, -14), 15), x2 = min(max(x - x1, -14), 15);
+        f1 = __half2half2(__ushort_as_half((unsigned short)((x1 + 15) << 10)));
+        f2 = __half2half2(__ushort_as_half((unsigned short)((x2 + 15) << 10)));
+        const uint32_t m = e == 255 || e == 0 ? cb : (cb & 0x807Fu) | 0x3F80u;   // c's sign and significand
+        *reinterpret_cast<__half*>(tab + PL * NG * 512 + col * 4 + hf * 2) = __float2half_rn(bf16_bits_to_f32(m));
       }
 #pragma unroll
       for (int pl = 0; pl < PL; ++pl) {
@@ -892,14 +892,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + (pl ? C::R_CODES : C::A_CODES)) + tok * NG;
 #pragma unroll
         for (int gi = 0; gi < NG; ++gi) {
-          const float2 so = e4m3x2_to_f32x2(meta[gi]);
-          const float g = pl ? 1.f : f;
-          __half sh = half_sat(so.x * g);
-          __half kh = half_sat(fmaf(pl ? -4.f : -16.f, __half2float(sh), so.y * g));
-          if (!on) sh = kh = __ushort_as_half(0);
+          __half2 so = e4m3_pair(on ? meta[gi] : (uint16_t)0);
+          if (NRES && pl == 0) so = __hmul2(__hmul2(so, f1), f2);
           uint8_t* e = tab + ((pl * NG + gi) * 64 + col) * 8 + hf * 2;
-          *reinterpret_cast<__half*>(e) = sh;
-          *reinterpret_cast<__half*>(e + 4) = kh;
+          *reinterpret_cast<__half*>(e) = __low2half(so);
+          *reinterpret_cast<__half*>(e + 4) =
+              __hfma(__low2half(so), __float2half_rn(pl ? -4.f : -16.f), __high2half(so));
         }
       }
       wg_sync(2);
@@ -911,7 +909,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
           const uint8_t* tile = pl ? s + C::RV : s + C::AV;
           const uint4* tb = reinterpret_cast<const uint4*>(tab + (pl * NG + lt / GS) * 64 * 8);
           const uint4* cm = reinterpret_cast<const uint4*>(tab + PL * NG * 512);   // significands of c
-#pragma unroll
+#pragma unroll 1
           for (int c4 = 0; c4 < 4; ++c4) {   // 32 tokens: 16 columns
             uint32_t r[16];
             const uint8_t* row = tile + (c4 >> 1) * (pl ? C::R_TILE : C::A_TILE) + lt * (pl ? 16 : 32);
