@@ -17,15 +17,19 @@
 // Roles (14 warps): K dequantizer, softmax, V dequantizer (4 warps each, one per 32
 // lanes), one copy warp, one MMA warp.
 //
-// Dequantization: a code moved into the mantissa of 16.0 (INT4) or 4.0 (INT2) is the
-// exact f16 16 + code; one fused multiply-add with (s, o - 16 s) gives s code + o rounded
-// once: shift, mask, multiply-add per two elements.
+// Dequantization: an f16 whose bits are an integer n < 1024 has the value n 2^-24, so masking a
+// code word leaves codes times 2^(p - 24), p the field's first bit; one fused multiply-add with
+// (s 2^(24 - p - k), o 2^-k) gives (s code + o) 2^-k.  k = 15: every E4M3 s and o stays in f16's
+// range, and being multiples of 2^-9 they and the sums stay exact.  (Logic and shift instructions
+// run at half rate here and bound this kernel: 7 of them a word of 8 codes, 11 of 16.)
 //
 // Softmax: a token's scores sit in one lane, a query's across the lanes.  The running
 // reference of a query therefore moves only when some score exceeds it by 2^8 (the first
 // step, then rarely): weights stay below 2^14, in f16 range, and O is rescaled in
 // tensor memory then.  Sums stay in the lanes' registers until the unit ends.
 #pragma once
+
+#include <type_traits>
 
 #include <cuda_fp8.h>
 
@@ -125,6 +129,16 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) 
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// 16 lanes x 32 columns: lane l of the warp holds, of rows l / 4 and l / 4 + 8 (registers + 2), the
+// columns 8 j + 2 (l % 4) and the next (registers 4 j, 4 j + 1)
+__device__ __forceinline__ void tc_st_frag(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
@@ -162,7 +176,7 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 
 // The wait behind a failed first try: until the phase ends, or the CTA gives up (out of
 // line: it is used in some thirty places, and instruction fetch bounds the streaming kernel)
-__device__ __noinline__ bool tree_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+__device__ __forceinline__ bool tree_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                             int32_t* status) {
   const unsigned long long t0 = global_ns();
   while (!*abort_flag) {
@@ -197,24 +211,42 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// INT4 word: r[s] = (16 + code at bits 4s, 16 + code at bits 4s + 16)
+// INT4 word: r[s] = 2^-20 times the codes at bits 4 s and 4 s + 16
 __device__ __forceinline__ void codes4(uint32_t w, uint32_t (&r)[4]) {
-  r[0] = ((w << 6) & 0x03C003C0u) | 0x4C004C00u;
-  r[1] = ((w << 2) & 0x03C003C0u) | 0x4C004C00u;
-  r[2] = ((w >> 2) & 0x03C003C0u) | 0x4C004C00u;
-  r[3] = ((w >> 6) & 0x03C003C0u) | 0x4C004C00u;
+  r[0] = (w << 4) & 0x00F000F0u;
+  r[1] = w & 0x00F000F0u;
+  r[2] = (w >> 4) & 0x00F000F0u;
+  r[3] = (w >> 8) & 0x00F000F0u;
 }
-// INT2 word: r[4 i + m] = (4 + code at bits 8 i + 2 m, 4 + code at bits 8 i + 2 m + 16), i = 0, 1
+// INT2 word: r[4 i + m] = 2^-22, 2^-22, 2^-20, 2^-18 (m = 0 .. 3) times the codes at bits 8 i + 2 m
+// and 16 further, i = 0, 1
 __device__ __forceinline__ void codes2(uint32_t w, uint32_t (&r)[8]) {
-  r[0] = ((w << 8) & 0x03000300u) | 0x44004400u;
-  r[1] = ((w << 6) & 0x03000300u) | 0x44004400u;
-  r[2] = ((w << 4) & 0x03000300u) | 0x44004400u;
-  r[3] = ((w << 2) & 0x03000300u) | 0x44004400u;
-  r[4] = (w & 0x03000300u) | 0x44004400u;
-  r[5] = ((w >> 2) & 0x03000300u) | 0x44004400u;
-  r[6] = ((w >> 4) & 0x03000300u) | 0x44004400u;
-  r[7] = ((w >> 6) & 0x03000300u) | 0x44004400u;
+  r[0] = (w << 2) & 0x000C000Cu;
+  r[1] = w & 0x000C000Cu;
+  r[2] = w & 0x00300030u;
+  r[3] = w & 0x00C000C0u;
+  r[4] = (w >> 6) & 0x000C000Cu;
+  r[5] = (w >> 8) & 0x000C000Cu;
+  r[6] = (w >> 8) & 0x00300030u;
+  r[7] = (w >> 8) & 0x00C000C0u;
 }
+// f16 2^e, -14 <= e <= 15
+__device__ __forceinline__ __half half_pow2(int e) { return __ushort_as_half((unsigned short)((e + 15) << 10)); }
+constexpr int kScaleK = 15;    // dequantized operands carry 2^-15 (V's anchor under a coefficient: 2^-7)
+
+// Channel in the low half of column col of a K' row (the other half: 4 further in the anchor's
+// part, 8 in the residual's): the order in which the dequantizers leave them.
+template <int D>
+__device__ __forceinline__ int k_channel(int col, bool res) {
+  if (D != 128) return res ? (col >> 3) * 16 + (col & 7) : (col >> 2) * 8 + (col & 3);
+  const int j = col >> 3, t = (col >> 1) & 3, e = col & 1;   // thread t of four holds channels 32 t ..
+  return 32 * t + (res ? (j >> 2) * 16 + 2 * (j & 3) + e : (j >> 1) * 8 + 2 * (j & 1) + e);
+}
+// Row of token tau's weights in P, that is the place of its column half in V'^T
+__device__ __forceinline__ int v_slot(int tau) {
+  return 16 * ((tau & 31) >> 2) + 4 * (tau >> 5) + 2 * (tau & 1) + ((tau >> 1) & 1);
+}
+
 // Per-CTA view of the call's work, in shared memory: steps before row b, steps of a unit of row b
 struct TreeRowsShared {
   int pre[kTreeRows + 1];
@@ -340,7 +372,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (lane < D / 4) q_s[warp][4 * lane + i] = ldexpf(x[i], 11 - e);
-    if (lane == 0) a.q_scale[(size_t)unit * NB + r] = ldexpf(a.qscale, e - 11);
+    if (lane == 0) a.q_scale[(size_t)unit * NB + r] = ldexpf(a.qscale, e - 11 + kScaleK);
   }
   __syncthreads();
   if (NRES && hadamard) {
@@ -393,8 +425,8 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
     const float* x = pl ? r_s[qi] : q_s[qi];
     uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {   // slots 8 c + 2 j, + 1
-      const int lo = pl ? (c >> 1) * 16 + (c & 1) * 4 + j : c * 8 + j;
+    for (int j = 0; j < 4; ++j) {
+      const int lo = k_channel<D>(4 * c + j, pl != 0);
       w[j] = f16x2(x[lo], x[lo + (pl ? 8 : 4)]);
     }
     const int r = q0 + qi, kb = c >> 3, chunk = c & 7;
@@ -613,56 +645,115 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     }
     __syncwarp();
   } else if (warp < 4) {
-    // ================= K: one token a lane =================
-    const int tok = tid & 63, tau = tid >> 6;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    // ================= K: rows of tokens =================
+    const int tau = warp >> 1;                              // the warp's tile of the step
+    const int t4 = lane & 3, base = warp * 32;
+    const uint32_t lanes = tmem + ((uint32_t)base << 16);
     for (int it = 0; it < n_it; ++it) {
       const int st = it % ST;
       wait_warp(&full_bar[st], (it / ST) & 1);
       const uint8_t* s = stages + st * C::STAGE;
-      const bool on = tid < valid_of(cur);
+      const int nv = valid_of(cur);
 #pragma unroll
       for (int pl = 0; pl < PL; ++pl) {
         const uint8_t* tile = pl ? s + C::RK + tau * C::R_TILE : s + tau * C::A_TILE;
-        const uint8_t* row = tile + tok * (pl ? D / 4 : D / 2);
-        const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + (pl ? C::R_CODES : C::A_CODES)) + tok * NG;
-        // (s, s) and (o - 16 s or o - 4 s, twice) of group gi
-        auto consts = [&](int gi, __half2* sc, __half2* kc) {
-          const __half2 so = e4m3_pair(on ? meta[gi] : (uint16_t)0);
-          *sc = __low2half2(so);
-          *kc = __half2half2(__hfma(__low2half(so), __float2half_rn(pl ? -4.f : -16.f), __high2half(so)));
+        const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + (pl ? C::R_CODES : C::A_CODES));
+        // the multiplier (residual: of the fields at bit 2, 4, 6) and the addend of group gi of the
+        // tile's token `tok`; behind the row's end zeros, so that what lies there stays finite
+        struct Consts { __half2 m[3], o; };
+        auto consts = [&](int tok, int gi) {
+          __half2 so = e4m3_pair(tau * kTile + tok < nv ? meta[tok * NG + gi] : (uint16_t)0);
+          so = __hmul2(so, __halves2half2(half_pow2(24 - 4 - kScaleK), __ushort_as_half(0x0200)));   // 2^5, 2^-15
+          Consts c;
+          const __half2 m = __low2half2(so);
+          c.o = __high2half2(so);
+          c.m[0] = pl ? __hmul2(m, __half2half2(half_pow2(2))) : m;
+          c.m[1] = m;
+          c.m[2] = pl ? __hmul2(m, __half2half2(half_pow2(-2))) : m;
+          return c;
         };
         wait_warp(&kempty_bar[pl], (it & 1) ^ 1);
         tc_after();
-#pragma unroll 1   // straight-line code for every chunk would stream through the instruction caches
-        for (int c = 0; c < D / 32; ++c) {   // 32 channels: 16 columns
-          uint32_t r[16];
-          if (pl == 0) {
-            const uint4 w = reinterpret_cast<const uint4*>(row)[c];
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-            __half2 sc, kc;
+        if (D == 128) {
+          // four lanes share a token, 32 channels each: contiguous shared-memory reads
+#pragma unroll 1   // straight-line code for every part would stream through the instruction caches
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t w[2][4];
+            Consts k2[2][32 / GS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (i * 8 % GS == 0) consts(c * (32 / GS) + i * 8 / GS, &sc, &kc);
-              uint32_t v[4];
-              codes4(ww[i], v);
+            for (int k = 0; k < 2; ++k) {
+              const int tok = (base & 63) + 16 * hh + 8 * k + (lane >> 2);
+              if (pl == 0) {
+                const uint4 v = *reinterpret_cast<const uint4*>(tile + tok * (D / 2) + t4 * 16);
+                w[k][0] = v.x; w[k][1] = v.y; w[k][2] = v.z; w[k][3] = v.w;
+              } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(tile + tok * (D / 4) + t4 * 8);
+                w[k][0] = v.x; w[k][1] = v.y;
+              }
 #pragma unroll
-              for (int j = 0; j < 4; ++j) r[4 * i + j] = h2u(__hfma2(u2h(v[j]), sc, kc));
+              for (int c = 0; c < 32 / GS; ++c) k2[k][c] = consts(tok, t4 * (32 / GS) + c);
             }
-          } else {
-            const uint2 w = reinterpret_cast<const uint2*>(row)[c];
-            const uint32_t ww[2] = {w.x, w.y};
-            __half2 sc, kc;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (i * 16 % GS == 0) consts(c * (32 / GS) + i * 16 / GS, &sc, &kc);
-              uint32_t v[8];
-              codes2(ww[i], v);
+            for (int c = 0; c < 2; ++c) {
+              constexpr int G1 = 32 / GS - 1;
+              uint32_t r[16];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) r[8 * i + j] = h2u(__hfma2(u2h(v[j]), sc, kc));
+              for (int k = 0; k < 2; ++k) {
+                const Consts& q = k2[k][c & G1];
+                if (pl == 0) {
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    uint32_t v[4];
+                    codes4(w[k][2 * c + i], v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                      r[4 * (2 * i + (j >> 1)) + 2 * k + (j & 1)] = h2u(__hfma2(u2h(v[j]), q.m[1], q.o));
+                  }
+                } else {
+                  uint32_t v[8];
+                  codes2(w[k][c], v);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j)
+                    r[4 * (j >> 1) + 2 * k + (j & 1)] = h2u(__hfma2(u2h(v[j]), q.m[(j & 3) < 2 ? 0 : (j & 3) - 1], q.o));
+                }
+              }
+              tc_st_frag(lanes + ((uint32_t)(16 * hh) << 16) + (pl ? C::KR : C::KA) + 32 * c, r);
             }
           }
-          tc_st16(lanes + (pl ? C::KR : C::KA) + 16 * c, r);
+        } else {
+          // width 96 does not split into four; one token a lane (rows of 48 bytes: no bank conflicts)
+          const int tok = tid & 63;
+          const uint8_t* row = tile + tok * (pl ? D / 4 : D / 2);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {   // 32 channels: 16 columns
+            uint32_t r[16];
+            Consts q;
+            if (pl == 0) {
+              const uint4 w = reinterpret_cast<const uint4*>(row)[c];
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (i * 8 % GS == 0) q = consts(tok, c * (32 / GS) + i * 8 / GS);
+                uint32_t v[4];
+                codes4(ww[i], v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[4 * i + j] = h2u(__hfma2(u2h(v[j]), q.m[1], q.o));
+              }
+            } else {
+              const uint2 w = reinterpret_cast<const uint2*>(row)[c];
+              const uint32_t ww[2] = {w.x, w.y};
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if (i * 16 % GS == 0) q = consts(tok, c * (32 / GS) + i * 16 / GS);
+                uint32_t v[8];
+                codes2(ww[i], v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  r[8 * i + j] = h2u(__hfma2(u2h(v[j]), q.m[(j & 3) < 2 ? 0 : (j & 3) - 1], q.o));
+              }
+            }
+            tc_st16(lanes + (pl ? C::KR : C::KA) + 16 * c, r);
+          }
         }
         tc_wait_st();
         tc_before();
@@ -676,7 +767,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     // ================= softmax: one token a lane =================
     const int lt = tid - 128, tok = lt & 63, tau = lt >> 6, w4 = warp - 4;
     const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
-    const int slot = (lt & ~3) + ((lt & 1) << 1 | ((lt >> 1) & 1));   // the token's row of P (the V codes' order)
+    const int slot = v_slot(lt);
+    constexpr bool KEEP = NB <= 32;
     float l[NB];
     pdl_wait();
     for (int it = 0; it < n_it; ++it) {
@@ -728,13 +820,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         }
       };
       float top = -INFINITY;
+      float2 kept[KEEP ? NB / 2 : 1];     // relative scores, where they fit the registers
 #pragma unroll
       for (int ch = 0; ch < NB / 16; ++ch) {
         float2 y[8];
         scores(ch, y);
         relative(ch, y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(y[i].x, y[i].y));
+        for (int i = 0; i < 8; ++i) {
+          top = fmaxf(top, fmaxf(y[i].x, y[i].y));
+          if (KEEP) kept[(KEEP ? 8 * ch + i : 0)] = y[i];
+        }
       }
       if (wg_any(1, on && top > kTop)) {
         // move the references to this step's maxima where those are higher
@@ -775,6 +871,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
           }
           tc_wait_st();
         }
+        if (KEEP) {
+#pragma unroll
+          for (int ch = 0; ch < NB / 16; ++ch) {
+            float2 y[8];
+            scores(ch, y);
+            relative(ch, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) kept[(KEEP ? 8 * ch + i : 0)] = y[i];
+          }
+        }
       }
       // weights
       wait_warp(&pempty_bar[it & 1], ((it >> 1) & 1) ^ 1);
@@ -782,8 +888,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
 #pragma unroll
       for (int ch = 0; ch < NB / 16; ++ch) {
         float2 y[8];
-        scores(ch, y);
-        relative(ch, y);
+        if (KEEP) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = kept[(KEEP ? 8 * ch + i : 0)];
+        } else {
+          scores(ch, y);
+          relative(ch, y);
+        }
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -858,33 +969,40 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       if (it + 1 < n_it) cur.next(rows_s, per);
     }
   } else {
-    // ================= V: one channel a lane =================
+    // ================= V: rows of channels =================
     const int lt = tid - 256, w4 = warp - 8;
     const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
-    const int col = 2 * (lt >> 2) + (lt & 1), hf = (lt >> 1) & 1;   // the token's place among the constants
+    const int col = v_slot(lt) >> 1, hf = v_slot(lt) & 1;   // the token's place among the constants
+    const int t4 = lane & 3;                                // the lane's 32 tokens: 32 t4 ..
     const int tok = lt & 63, tau = lt >> 6;
+    // the field of this token in residual words starts at bit 2, 2, 4, 6 (as codes2 leaves it); its
+    // multiplier is that many powers of two below the one of bit 4
+    const int quad = (lt & 31) >> 2;
+    const __half2 field = __halves2half2(half_pow2((quad & 3) < 2 ? 2 : ((quad & 3) == 2 ? 0 : -2)), half_pow2(0));
+    const __half2 to_k = __halves2half2(half_pow2(24 - 4 - kScaleK), __ushort_as_half(0x0200));     // 2^5, 2^-15
     for (int it = 0; it < n_it; ++it) {
       const int st = it % ST;
       wait_warp(&full_bar[st], (it / ST) & 1);
       const uint8_t* s = stages + st * C::STAGE;
       const bool on = lt < valid_of(cur);
       wg_sync(2);   // the previous step's constants are used up
-      // Constants of this lane's token: (f s, f o - 16 f s) for the anchor, (s, o - 4 s) for the
-      // residual.  The coefficient c = m f, f a power of two and 1 <= |m| < 2: powers of two
-      // leave the constants exact, and m multiplies the finished f (s code + o), so that a
-      // value is rounded relative to itself and not to its group's range.
-      __half2 f1 = __half2half2(__ushort_as_half(0x3C00)), f2 = f1;
+      // Constants of this lane's token.  The anchor's coefficient c = m f, f a power of two and
+      // 1 <= |m| < 2: f goes into the constants, where powers of two are exact, and m multiplies the
+      // finished f (s code + o), so that a value is rounded relative to itself and not to its group's
+      // range.  That product carries 2^-7: its operands 2^-13 and m 2^6.
+      __half2 f1 = __half2half2(half_pow2(0)), f2 = f1;
       if (NRES) {
         uint16_t cb =
             *reinterpret_cast<const uint16_t*>(s + C::RV + tau * C::R_TILE + C::R_CODES + C::META + tok * 2);
         if ((cb & 0x7F80) == 0 || !on) cb = 0;                          // a subnormal c counts as zero
         const int e = (cb >> 7) & 0xFF;
-        // f = 2^(e - 127) as two factors of f16 range; infinite and NaN c keep f = 1
-        const int x = e == 0 || e == 255 ? 0 : e - 127, x1 = min(max(x, -14), 15), x2 = min(max(x - x1, -14), 15);
-        f1 = __half2half2(__ushort_as_half((unsigned short)((x1 + 15) << 10)));
-        f2 = __half2half2(__ushort_as_half((unsigned short)((x2 + 15) << 10)));
+        // 4 f = 2^(e - 125) as two factors of f16 range; infinite and NaN c keep f = 1
+        const int x = (e == 0 || e == 255 ? 0 : e - 127) + 2, x1 = min(max(x, -14), 15), x2 = min(max(x - x1, -14), 15);
+        f1 = __half2half2(half_pow2(x1));
+        f2 = __half2half2(half_pow2(x2));
         const uint32_t m = e == 255 || e == 0 ? cb : (cb & 0x807Fu) | 0x3F80u;   // c's sign and significand
-        *reinterpret_cast<__half*>(tab + PL * NG * 512 + col * 4 + hf * 2) = __float2half_rn(bf16_bits_to_f32(m));
+        *reinterpret_cast<__half*>(tab + PL * NG * 512 + col * 4 + hf * 2) =
+            __float2half_rn(bf16_bits_to_f32(m) * 64.f);
       }
 #pragma unroll
       for (int pl = 0; pl < PL; ++pl) {
@@ -892,12 +1010,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + (pl ? C::R_CODES : C::A_CODES)) + tok * NG;
 #pragma unroll
         for (int gi = 0; gi < NG; ++gi) {
-          __half2 so = e4m3_pair(on ? meta[gi] : (uint16_t)0);
-          if (NRES && pl == 0) so = __hmul2(__hmul2(so, f1), f2);
+          __half2 so = __hmul2(e4m3_pair(on ? meta[gi] : (uint16_t)0), to_k);
+          if (pl) so = __hmul2(so, field);
+          else if (NRES) so = __hmul2(__hmul2(so, f1), f2);
           uint8_t* e = tab + ((pl * NG + gi) * 64 + col) * 8 + hf * 2;
           *reinterpret_cast<__half*>(e) = __low2half(so);
-          *reinterpret_cast<__half*>(e + 4) =
-              __hfma(__low2half(so), __float2half_rn(pl ? -4.f : -16.f), __high2half(so));
+          *reinterpret_cast<__half*>(e + 4) = __high2half(so);
         }
       }
       wg_sync(2);
@@ -906,50 +1024,58 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         wait_warp(&vempty_bar[pl], (it & 1) ^ 1);
         tc_after();
         if (D == 128 || w4 < 3) {
-          const uint8_t* tile = pl ? s + C::RV : s + C::AV;
-          const uint4* tb = reinterpret_cast<const uint4*>(tab + (pl * NG + lt / GS) * 64 * 8);
-          const uint4* cm = reinterpret_cast<const uint4*>(tab + PL * NG * 512);   // significands of c
+          // four lanes share a channel, 32 tokens each; a lane has four channels (l / 4 + 8 k), so that
+          // a constant read from shared memory serves four (groups of 16 channels: two)
+          const uint8_t* row = (pl ? s + C::RV + (t4 >> 1) * C::R_TILE : s + C::AV + (t4 >> 1) * C::A_TILE) +
+                               (w4 * 32 + (lane >> 2)) * (pl ? 16 : 32) + (t4 & 1) * (pl ? 8 : 16);
+          const uint4* tb = reinterpret_cast<const uint4*>(tab + (pl * NG + w4 * (32 / GS)) * 512) + t4;
+          const uint2* cm = reinterpret_cast<const uint2*>(tab + PL * NG * 512) + t4;   // significands of c
 #pragma unroll 1
-          for (int c4 = 0; c4 < 4; ++c4) {   // 32 tokens: 16 columns
-            uint32_t r[16];
-            const uint8_t* row = tile + (c4 >> 1) * (pl ? C::R_TILE : C::A_TILE) + lt * (pl ? 16 : 32);
-            if (pl == 0) {
-              const uint4 w = reinterpret_cast<const uint4*>(row)[c4 & 1];
-              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          for (int c = 0; c < 2; ++c) {        // 16 of the lane's tokens: four pairs of columns
+            uint4 kq[4];
+            uint2 mq[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {    // word: tokens 8 i ..; columns 4 i ..
-                uint32_t v[4];
-                codes4(ww[i], v);
-                // masks leave tokens (0, 2), (4, 6), (1, 3), (5, 7); columns hold (0, 2), (1, 3), (4, 6), (5, 7)
-                const uint4 k0 = tb[c4 * 8 + 2 * i], k1 = tb[c4 * 8 + 2 * i + 1];
-                r[4 * i] = h2u(__hfma2(u2h(v[0]), u2h(k0.x), u2h(k0.y)));
-                r[4 * i + 1] = h2u(__hfma2(u2h(v[2]), u2h(k0.z), u2h(k0.w)));
-                r[4 * i + 2] = h2u(__hfma2(u2h(v[1]), u2h(k1.x), u2h(k1.y)));
-                r[4 * i + 3] = h2u(__hfma2(u2h(v[3]), u2h(k1.z), u2h(k1.w)));
-                if (NRES) {
-                  const uint4 m = cm[c4 * 4 + i];
-                  r[4 * i] = h2u(__hmul2(u2h(r[4 * i]), u2h(m.x)));
-                  r[4 * i + 1] = h2u(__hmul2(u2h(r[4 * i + 1]), u2h(m.y)));
-                  r[4 * i + 2] = h2u(__hmul2(u2h(r[4 * i + 2]), u2h(m.z)));
-                  r[4 * i + 3] = h2u(__hmul2(u2h(r[4 * i + 3]), u2h(m.w)));
+            for (int hh = 0; hh < 2; ++hh) {
+              if (hh == 0 || GS == 16) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) kq[j] = tb[(GS == 16 ? hh * 32 : 0) + 16 * c + 4 * j];
+              }
+              if (NRES && pl == 0 && hh == 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mq[j] = cm[16 * c + 4 * j];
+              }
+              uint32_t r[16];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint8_t* p = row + (16 * hh + 8 * k) * (pl ? 16 : 32) + c * (pl ? 4 : 8);
+                if (pl == 0) {
+                  const uint2 w = *reinterpret_cast<const uint2*>(p);
+                  const uint32_t ww[2] = {w.x, w.y};
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    uint32_t v[4];
+                    codes4(ww[i], v);          // v[x]: tokens (0, 2) of quad x & 1 from token x >> 1
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                      const int j = 2 * i + (x & 1), e = x >> 1;
+                      __half2 z = __hfma2(u2h(v[x]), u2h(e ? kq[j].z : kq[j].x), u2h(e ? kq[j].w : kq[j].y));
+                      if (NRES) z = __hmul2(z, u2h(e ? mq[j].y : mq[j].x));
+                      r[4 * j + 2 * k + e] = h2u(z);
+                    }
+                  }
+                } else {
+                  uint32_t v[8];
+                  codes2(*reinterpret_cast<const uint32_t*>(p), v);   // v[4 e + j]: quad j from token e
+#pragma unroll
+                  for (int x = 0; x < 8; ++x) {
+                    const int j = x & 3, e = x >> 2;
+                    r[4 * j + 2 * k + e] =
+                        h2u(__hfma2(u2h(v[x]), u2h(e ? kq[j].z : kq[j].x), u2h(e ? kq[j].w : kq[j].y)));
+                  }
                 }
               }
-            } else {
-              const uint2 w = reinterpret_cast<const uint2*>(row)[c4 & 1];
-              const uint32_t ww[2] = {w.x, w.y};
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {    // word: tokens 16 i ..; columns 8 i ..
-                uint32_t v[8];
-                codes2(ww[i], v);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {  // quad m: columns (0, 2), (1, 3)
-                  const uint4 k0 = tb[c4 * 8 + 4 * i + m];
-                  r[8 * i + 2 * m] = h2u(__hfma2(u2h(v[m]), u2h(k0.x), u2h(k0.y)));
-                  r[8 * i + 2 * m + 1] = h2u(__hfma2(u2h(v[4 + m]), u2h(k0.z), u2h(k0.w)));
-                }
-              }
+              tc_st_frag(lanes + ((uint32_t)(16 * hh) << 16) + (pl ? C::VR : C::VA) + 32 * c, r);
             }
-            tc_st16(lanes + (pl ? C::VR : C::VA) + 16 * c4, r);
           }
           tc_wait_st();
         }
@@ -1119,6 +1245,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, int ctas) {
     for (int i = 0; i < kMergeQ; ++i) {
       f[i] = exp2f(__ldcg(p + qo + i) - mine[i]);
       l[i] = fmaf(f[i], __ldcg(p + NB + qo + i), l[i]);
+      f[i] *= NRES ? 128.f : 32768.f;   // the operands' power of two
     }
     if (tid < D) {
 #pragma unroll
@@ -1131,10 +1258,10 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, int ctas) {
         if (NRES) {
           const float4 y =
               __ldcg(reinterpret_cast<const float4*>(p + 2 * NB) + (size_t)(NB / 4 + qo / 4 + i4) * D + tid);
-          orr[4 * i4] = fmaf(f[4 * i4], y.x, orr[4 * i4]);
-          orr[4 * i4 + 1] = fmaf(f[4 * i4 + 1], y.y, orr[4 * i4 + 1]);
-          orr[4 * i4 + 2] = fmaf(f[4 * i4 + 2], y.z, orr[4 * i4 + 2]);
-          orr[4 * i4 + 3] = fmaf(f[4 * i4 + 3], y.w, orr[4 * i4 + 3]);
+          orr[4 * i4] = fmaf(256.f * f[4 * i4], y.x, orr[4 * i4]);
+          orr[4 * i4 + 1] = fmaf(256.f * f[4 * i4 + 1], y.y, orr[4 * i4 + 1]);
+          orr[4 * i4 + 2] = fmaf(256.f * f[4 * i4 + 2], y.z, orr[4 * i4 + 2]);
+          orr[4 * i4 + 3] = fmaf(256.f * f[4 * i4 + 3], y.w, orr[4 * i4 + 3]);
         }
       }
     }
