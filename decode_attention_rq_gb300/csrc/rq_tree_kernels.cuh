@@ -174,19 +174,22 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// The wait behind a failed first try: until the phase ends, or the CTA gives up (out of
-// line: it is used in some thirty places, and instruction fetch bounds the streaming kernel)
-__device__ __forceinline__ bool tree_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                            int32_t* status) {
-  const unsigned long long t0 = global_ns();
-  while (!*abort_flag) {
-    if (mbar_try_wait_sleep(bar, parity)) return true;
-    if (global_ns() - t0 > kWaitNs) {
-      *abort_flag = 1;
-      atomicExch(&status[0], 1);
-    }
-  }
-  return false;
+// Waits for a phase: kTries - `from` tries at most, false when none found it complete.  A failing
+// try lasts up to about 1.4 us, so that all of them take some seconds.  One short instruction
+// sequence with nothing to jump over when the first try succeeds: with all SMs fetching, the
+// streaming kernel is bound by instruction fetch as soon as the code of its roles' steps exceeds
+// the 32 KB instruction cache of an SM (1.2 -> 3.2 clocks an instruction).
+constexpr uint32_t kTries = 1u << 21;
+__device__ __forceinline__ bool tree_try(uint64_t* bar, uint32_t parity, uint32_t from) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, %3;\n\t"
+      "TRY:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tadd.u32 n, n, 1;\n\t"
+      "setp.lt.and.u32 q, n, %4, !p;\n\t@q bra TRY;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(from), "n"(kTries)
+      : "memory");
+  return ok != 0;
 }
 
 // ---- f16 pairs ---------------------------------------------------------------------
@@ -448,9 +451,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
   __shared__ __align__(16) float f_s[NB];
   __shared__ float wred_s[4][NB];
   __shared__ uint32_t tmem_s;
-  __shared__ volatile int abort_s;
+  // per step (eight in flight at most): tokens in use | first, last of its unit << 8, 9; the unit
+  __shared__ int2 info_s[8];
 
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  // aligned by an offset, not by a cast: the compiler keeps the address space (shared, not generic, loads)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* q_img = smem;                                  // two query operands
   uint8_t* p_buf = q_img + 2 * C::IMG;                    // two weight buffers
   uint8_t* stages = p_buf + 2 * C::PBUF;
@@ -470,7 +475,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       mbar_init(&pfull_bar[i], 4); mbar_init(&pempty_bar[i], 1);
     }
     mbar_init(&drain_bar, 1);
-    abort_s = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -489,94 +493,90 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
   }
   __syncthreads();
   tc_after();
-  const uint32_t tmem = tmem_s;
+  constexpr uint32_t tmem = 0;   // all 512 columns are this CTA's, from column 0 (tc_alloc wrote tmem_s = 0)
   pdl_launch_dependents();
 
-  // Waits are bounded.  Past the limit the CTA gives up: the copy and the MMA warp stop
-  // and let what they issued finish; the other roles run on to their end without
-  // waiting (their warps share named barriers, so none may leave alone).
+  // Waits are bounded.  A warp that gave up sets the status word; the copy warp then stops, the
+  // other roles run on to their end, one try a wait (their warps share named barriers, so none
+  // may leave alone).  What they compute is lost, every address stays as planned.
+  uint32_t from = 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return mbar_try_wait(bar, parity) || tree_wait_long(bar, parity, &abort_s, a.status);
+    if (tree_try(bar, parity, from)) return true;
+    from = kTries - 1;
+    a.status[0] = 1;
+    return false;
   };
   // the same by a whole warp, which goes on together (the tcgen05 loads and stores are warp-wide)
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
     (void)wait(bar, parity);
     __syncwarp();
   };
-  // the step's tokens in the cache, all warps agree
-  auto valid_of = [&](const TreeCursor& c) { return min(kTreeStep, rows_s.len[c.b] - c.step * kTreeStep); };
-
-  TreeCursor cur;
-  cur.seek(rows_s, a.batch, u0);
-
   if (warp == 12) {
     // ================= copies =================
     if (lane == 0) {
       const uint64_t pol = l2_evict_first_policy();
-      int seg = 0, issued = 0;
-      bool waited = false, ok = true;
-      auto load_q = [&](int unit) {
-        uint64_t* bar = &qfull_bar[seg & 1];
-        if (!(ok = wait(&qempty_bar[seg & 1], ((seg >> 1) & 1) ^ 1))) return;
-        mbar_arrive_expect_tx(bar, C::IMG);
-        bulk_g2s(q_img + (seg & 1) * C::IMG, a.packs + (size_t)unit * C::IMG, C::IMG, bar);
-        ++seg;
-      };
-      int pend_unit = -1;     // units whose operand waits for the prep kernel
-      for (int it = 0; it < n_it && ok; ++it) {
-        const int st = it % ST;
-        if (!(ok = wait(&empty_bar[st], ((it / ST) & 1) ^ 1))) break;
-        const int h = cur.in_row / a.nqb;
-        const int tiles = (valid_of(cur) + kTile - 1) / kTile, t0 = cur.step * 2;
+      TreeCursor cur;
+      cur.seek(rows_s, a.batch, u0);
+      int st = 0, seg = 0, q_unit = -1;          // q_unit: a unit whose query operand is still to be fetched
+      uint32_t par = 1;                          // parity of the stage's empty barrier
+      bool ok = true;
+      const uint8_t *pa = nullptr, *pr = nullptr;   // next K tile of the anchor, of the residual
+      int it = 0;
+#pragma unroll 1
+      for (; it < n_it; ++it) {
+        if (!(ok = wait(&empty_bar[st], par))) break;
+        const int left = rows_s.len[cur.b] - cur.step * kTreeStep, tiles = left > kTile ? 2 : 1, t0 = cur.step * 2;
+        const bool first = it == 0 || cur.step == 0, last = it + 1 == n_it || cur.step + 1 == cur.steps;
+        const int unit = cur.b * per + cur.in_row;
+        info_s[it & 7] = make_int2(min(left, kTreeStep) | (first ? 256 : 0) | (last ? 512 : 0), unit);
         uint8_t* dst = stages + st * C::STAGE;
-        mbar_arrive_expect_tx(&full_bar[st], tiles * (2 * C::A_TILE + NRES * 2 * C::R_TILE));
-        if (!a.g.paged) {      // the two tiles of a plane are neighbours
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            bulk_g2s_hint(dst + kv * C::AV, a.base + a.g.tile_offset(a.layer, a.group, cur.b, h, true, 0, kv, t0, 0),
-                          tiles * C::A_TILE, &full_bar[st], pol);
-            if (NRES)
-              bulk_g2s_hint(dst + (kv ? C::RV : C::RK),
-                            a.base + a.g.tile_offset(a.layer, a.group, cur.b, h, false, a.loop, kv, t0, 0),
-                            tiles * C::R_TILE, &full_bar[st], pol);
-          }
-        } else {
-#pragma unroll 1
-          for (int i = 0; i < tiles; ++i) {
-            int page = checked_page(a.g, raw_page(a.g, cur.b, t0 + i), a.status);
-            if (page < 0) page = 0;
-#pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv) {
-              bulk_g2s_hint(dst + kv * C::AV + i * C::A_TILE,
-                            a.base + a.g.tile_offset(a.layer, a.group, cur.b, h, true, 0, kv, t0 + i, page), C::A_TILE,
-                            &full_bar[st], pol);
-              if (NRES)
-                bulk_g2s_hint(dst + (kv ? C::RV : C::RK) + i * C::R_TILE,
-                              a.base + a.g.tile_offset(a.layer, a.group, cur.b, h, false, a.loop, kv, t0 + i, page),
-                              C::R_TILE, &full_bar[st], pol);
-            }
-          }
+        uint64_t* bar = &full_bar[st];
+        mbar_arrive_expect_tx(bar, tiles * (2 * C::A_TILE + NRES * 2 * C::R_TILE));
+        if (first) {
+          const int h = cur.in_row / a.nqb, t = a.g.paged ? 0 : t0;   // paged: page 0; a page adds page_bytes
+          pa = a.base + a.g.tile_offset(a.layer, a.group, cur.b, h, true, 0, 0, t, 0);
+          if (NRES) pr = a.base + a.g.tile_offset(a.layer, a.group, cur.b, h, false, a.loop, 0, t, 0);
+          q_unit = unit;
         }
-        ++issued;
-        if (it == 0 || cur.step == 0) {
-          const int unit = cur.b * per + cur.in_row;
-          if (!waited && it == 0 && n_it > 1 && cur.step + 1 < cur.steps && ST > 1) {
-            pend_unit = unit;    // one more step of the cache first: the prep kernel may still run
-          } else {
-            if (!waited) { pdl_wait(); waited = true; }
-            if (pend_unit >= 0) { load_q(pend_unit); pend_unit = -1; if (!ok) break; }
-            load_q(unit);
+        // contiguous: the two tiles of a plane are neighbours, one copy; paged: one a tile
+        int64_t off = 0, va = a.g.plane_a, vr = a.g.plane_r;
+        int n = a.g.paged ? 1 : tiles, i = 0;
+#pragma unroll 1
+        do {
+          if (a.g.paged) {
+            const int page = checked_page(a.g, raw_page(a.g, cur.b, t0 + i), a.status);
+            off = (int64_t)max(page, 0) * a.g.page_bytes;
+            va = C::A_TILE;
+            vr = C::R_TILE;
           }
-        } else if (pend_unit >= 0) {
-          if (!waited) { pdl_wait(); waited = true; }
-          load_q(pend_unit);
-          pend_unit = -1;
+          bulk_g2s_hint(dst, pa + off, n * C::A_TILE, bar, pol);
+          bulk_g2s_hint(dst + C::AV, pa + off + va, n * C::A_TILE, bar, pol);
+          if (NRES) {
+            bulk_g2s_hint(dst + C::RK - i * (C::A_TILE - C::R_TILE), pr + off, n * C::R_TILE, bar, pol);
+            bulk_g2s_hint(dst + C::RV - i * (C::A_TILE - C::R_TILE), pr + off + vr, n * C::R_TILE, bar, pol);
+          }
+          dst += C::A_TILE;
+          i += n;
+        } while (i < tiles);
+        if (!a.g.paged) {
+          pa += 2 * C::A_TILE;
+          if (NRES) pr += 2 * C::R_TILE;
+        }
+        if (++st == ST) { st = 0; par ^= 1; }
+        // the query operand; the call's first one a step late, as the prep kernel may still run
+        if (q_unit >= 0 && (it > 0 || last)) {
+          if (seg == 0) pdl_wait();
+          if (!(ok = wait(&qempty_bar[seg & 1], ((seg >> 1) & 1) ^ 1))) break;
+          uint64_t* qb = &qfull_bar[seg & 1];
+          mbar_arrive_expect_tx(qb, C::IMG);
+          bulk_g2s(q_img + (seg & 1) * C::IMG, a.packs + (size_t)q_unit * C::IMG, C::IMG, qb);
+          ++seg;
+          q_unit = -1;
         }
         if (it + 1 < n_it) cur.next(rows_s, per);
       }
       if (!ok) {   // copies in flight land before the CTA leaves
-        for (int i = max(0, issued - ST); i < issued; ++i)
-          (void)mbar_wait_bounded(&full_bar[i % ST], (i / ST) & 1);
+        for (int i = max(0, it - ST); i < it; ++i) (void)mbar_wait_bounded(&full_bar[i % ST], (i / ST) & 1);
         for (int i = max(0, seg - 2); i < seg; ++i) (void)mbar_wait_bounded(&qfull_bar[i & 1], (i >> 1) & 1);
       }
     }
@@ -586,74 +586,85 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     constexpr uint32_t id_s = tc_idesc(NB, false), id_o = tc_idesc(NB, true);
     const uint64_t q_desc = tc_desc(smem_u32(q_img)), p_desc = tc_desc(smem_u32(p_buf));
     int seg = -1;
-    bool ok = true, first_prev = false;
-    // O (+)= V'(j) P(j)
-    auto values = [&](int j, bool first) {
-      const uint64_t p0 = p_desc + (j & 1) * (C::PBUF >> 4);
-#pragma unroll
-      for (int pl = 0; pl < PL; ++pl) {
-        if (!(ok = ok && wait(&vfull_bar[pl], j & 1) && (pl || wait(&pfull_bar[j & 1], (j >> 1) & 1)))) return;
-        tc_after();
-        __syncwarp();
-        const uint32_t o = tmem + (pl ? C::OR : C::OA), v = tmem + (pl ? C::VR : C::VA);
-        if (elect_one()) {
-          if (first) tc_mma<false>(o, v, p0, id_o); else tc_mma<true>(o, v, p0, id_o);
-#pragma unroll
-          for (int k = 1; k < kTreeStep / 16; ++k) tc_mma<true>(o, v + 8 * k, p0 + k * (2048 >> 4), id_o);
-          tc_commit(&vempty_bar[pl]);
-          if (pl == PL - 1) tc_commit(&pempty_bar[j & 1]);
+    bool first = false;
+#pragma unroll 1
+    for (int it = 0; it <= n_it; ++it) {   // S of step it, then O of the step before
+      const bool first_prev = first;
+      if (it < n_it) {
+        wait(&kfull_bar[0], it & 1);
+        const int flags = info_s[it & 7].x;
+        first = (flags & 256) != 0;
+        if (first) {
+          ++seg;
+          wait(&qfull_bar[seg & 1], (seg >> 1) & 1);
         }
-        __syncwarp();
-      }
-    };
-    for (int it = 0; it < n_it; ++it) {
-      const bool first = it == 0 || cur.step == 0;
-      if (first) {
-        ++seg;
-        ok = ok && wait(&qfull_bar[seg & 1], (seg >> 1) & 1);
-      }
-      const uint64_t q0 = q_desc + (seg & 1) * (C::IMG >> 4);
-      ok = ok && wait(&sempty_bar[it % SB], ((it / SB) & 1) ^ 1);
+        wait(&sempty_bar[it % SB], ((it / SB) & 1) ^ 1);
 #pragma unroll
-      for (int pl = 0; pl < PL; ++pl) {
-        if (!(ok = ok && wait(&kfull_bar[pl], it & 1))) break;
-        tc_after();
-        __syncwarp();
-        const uint32_t d = tmem + C::S0 + (it % SB) * C::SCOLS + pl * NB, k0 = tmem + (pl ? C::KR : C::KA);
-        if (elect_one()) {
-          tc_mma<false>(d, k0, q0 + pl * (2 * C::QBLK >> 4), id_s);
-#pragma unroll
-          for (int k = 1; k < D / 16; ++k)
-            tc_mma<true>(d, k0 + 8 * k, q0 + ((pl * 2 + (k >> 2)) * C::QBLK >> 4) + (k & 3) * 2, id_s);
-          tc_commit(&kempty_bar[pl]);
-          if (pl == PL - 1) {
-            tc_commit(&sfull_bar[it % SB]);
-            if (it + 1 == n_it || cur.step + 1 == cur.steps) tc_commit(&qempty_bar[seg & 1]);
+        for (int pl = 0; pl < PL; ++pl) {
+          if (pl) wait(&kfull_bar[pl], it & 1);
+          tc_after();
+          __syncwarp();
+          if (elect_one()) {
+            const uint32_t d = tmem + C::S0 + (it % SB) * C::SCOLS + pl * NB, k0 = tmem + (pl ? C::KR : C::KA);
+            uint64_t qd = q_desc + (((seg & 1) * C::IMG + pl * 2 * C::QBLK) >> 4);
+            tc_mma<false>(d, k0, qd, id_s);
+            tc_mma<true>(d, k0 + 8, qd + 2, id_s);
+#pragma unroll 1
+            for (int k = 2; k < D / 16; k += 2) {
+              qd += (k & 3) == 0 ? (C::QBLK >> 4) - 4 : 4;
+              tc_mma<true>(d, k0 + 8 * k, qd, id_s);
+              tc_mma<true>(d, k0 + 8 * k + 8, qd + 2, id_s);
+            }
+            tc_commit(&kempty_bar[pl]);
+            if (pl == PL - 1) {
+              tc_commit(&sfull_bar[it % SB]);
+              if (flags & 512) tc_commit(&qempty_bar[seg & 1]);
+            }
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
-      if (ok && it > 0) values(it - 1, first_prev);
-      if (!ok) break;
-      first_prev = first;
-      if (it + 1 < n_it) cur.next(rows_s, per);
+      if (it > 0) {   // O (+)= V' P of step it - 1
+        const int j = it - 1;
+#pragma unroll
+        for (int pl = 0; pl < PL; ++pl) {
+          wait(&vfull_bar[pl], j & 1);
+          if (pl == 0) wait(&pfull_bar[j & 1], (j >> 1) & 1);
+          tc_after();
+          __syncwarp();
+          if (elect_one()) {
+            const uint32_t o = tmem + (pl ? C::OR : C::OA), v = tmem + (pl ? C::VR : C::VA);
+            const uint64_t p0 = p_desc + (j & 1) * (C::PBUF >> 4);
+            if (first_prev) tc_mma<false>(o, v, p0, id_o); else tc_mma<true>(o, v, p0, id_o);
+            tc_mma<true>(o, v + 8, p0 + (2048 >> 4), id_o);
+#pragma unroll 1
+            for (int k = 2; k < kTreeStep / 16; k += 2) {
+              tc_mma<true>(o, v + 8 * k, p0 + k * (2048 >> 4), id_o);
+              tc_mma<true>(o, v + 8 * k + 8, p0 + (k + 1) * (2048 >> 4), id_o);
+            }
+            tc_commit(&vempty_bar[pl]);
+            if (pl == PL - 1) tc_commit(&pempty_bar[j & 1]);
+          }
+          __syncwarp();
+        }
+      }
     }
-    if (ok) values(n_it - 1, first_prev);
-    if (__any_sync(0xffffffffu, !ok)) {   // products in flight end before tensor memory is given back
-      if (elect_one()) tc_commit(&drain_bar);
-      (void)mbar_wait_bounded(&drain_bar, 0);
-    }
+    // every product has ended before tensor memory is given back
+    if (elect_one()) tc_commit(&drain_bar);
+    wait(&drain_bar, 0);
     __syncwarp();
   } else if (warp < 4) {
     // ================= K: rows of tokens =================
     const int tau = warp >> 1;                              // the warp's tile of the step
     const int t4 = lane & 3, base = warp * 32;
     const uint32_t lanes = tmem + ((uint32_t)base << 16);
+    int st = 0;
+    uint32_t par = 0;
+#pragma unroll 1
     for (int it = 0; it < n_it; ++it) {
-      const int st = it % ST;
-      wait_warp(&full_bar[st], (it / ST) & 1);
+      wait_warp(&full_bar[st], par);
       const uint8_t* s = stages + st * C::STAGE;
-      const int nv = valid_of(cur);
+      const int nv = info_s[it & 7].x & 255;
 #pragma unroll
       for (int pl = 0; pl < PL; ++pl) {
         const uint8_t* tile = pl ? s + C::RK + tau * C::R_TILE : s + tau * C::A_TILE;
@@ -761,7 +772,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         if (lane == 0) mbar_arrive(&kfull_bar[pl]);
       }
       if (lane == 0) mbar_arrive(&empty_bar[st]);
-      if (it + 1 < n_it) cur.next(rows_s, per);
+      if (++st == ST) { st = 0; par ^= 1; }
     }
   } else if (warp < 8) {
     // ================= softmax: one token a lane =================
@@ -771,9 +782,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     constexpr bool KEEP = NB <= 32;
     float l[NB];
     pdl_wait();
+    int st = 0;
+    uint32_t par = 0;
+#pragma unroll 1
     for (int it = 0; it < n_it; ++it) {
-      const bool first = it == 0 || cur.step == 0;
-      const int unit = cur.b * per + cur.in_row;
+      if (NRES) wait_warp(&full_bar[st], par); else wait_warp(&sfull_bar[it % SB], (it / SB) & 1);
+      const int2 info = info_s[it & 7];
+      const bool first = (info.x & 256) != 0, on = lt < (info.x & 255);
+      const int unit = info.y;
       if (first) {
 #pragma unroll
         for (int i = 0; i < NB; ++i) l[i] = 0.f;
@@ -783,19 +799,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         }
         wg_sync(1);
       }
-      const int nv = valid_of(cur), st = it % ST;
-      const bool on = lt < nv;
       float c = 0.f;
       if (NRES) {
-        wait_warp(&full_bar[st], (it / ST) & 1);
         const uint16_t cb = *reinterpret_cast<const uint16_t*>(stages + st * C::STAGE + C::RK + tau * C::R_TILE +
                                                                C::R_CODES + C::META + tok * 2);
         c = on ? bf16_bits_to_f32(cb) : 0.f;
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty_bar[st]);
+        if (++st == ST) { st = 0; par ^= 1; }
+        wait_warp(&sfull_bar[it % SB], (it / SB) & 1);
       }
       const float2 c2 = make_float2(c, c);
-      wait_warp(&sfull_bar[it % SB], (it / SB) & 1);
       tc_after();
       const uint32_t s0 = lanes + C::S0 + (it % SB) * C::SCOLS;
       // score products of 16 queries with this lane's token
@@ -832,7 +846,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
           if (KEEP) kept[(KEEP ? 8 * ch + i : 0)] = y[i];
         }
       }
-      if (wg_any(1, on && top > kTop)) {
+      if (__builtin_expect(wg_any(1, on && top > kTop), 0)) {
         // move the references to this step's maxima where those are higher
 #pragma unroll
         for (int ch = 0; ch < NB / 16; ++ch) {
@@ -914,7 +928,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         mbar_arrive(&sempty_bar[it % SB]);
         mbar_arrive(&pfull_bar[it & 1]);
       }
-      if (it + 1 == n_it || cur.step + 1 == cur.steps) {
+      if (__builtin_expect((info.x & 512) != 0, 0)) {
         // the unit's state out
         wait_warp(&pempty_bar[it & 1], (it >> 1) & 1);
         tc_after();
@@ -966,7 +980,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         }
         wg_sync(1);
       }
-      if (it + 1 < n_it) cur.next(rows_s, per);
     }
   } else {
     // ================= V: rows of channels =================
@@ -980,11 +993,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     const int quad = (lt & 31) >> 2;
     const __half2 field = __halves2half2(half_pow2((quad & 3) < 2 ? 2 : ((quad & 3) == 2 ? 0 : -2)), half_pow2(0));
     const __half2 to_k = __halves2half2(half_pow2(24 - 4 - kScaleK), __ushort_as_half(0x0200));     // 2^5, 2^-15
+    int st = 0;
+    uint32_t par = 0;
+#pragma unroll 1
     for (int it = 0; it < n_it; ++it) {
-      const int st = it % ST;
-      wait_warp(&full_bar[st], (it / ST) & 1);
+      wait_warp(&full_bar[st], par);
       const uint8_t* s = stages + st * C::STAGE;
-      const bool on = lt < valid_of(cur);
+      const bool on = lt < (info_s[it & 7].x & 255);
       wg_sync(2);   // the previous step's constants are used up
       // Constants of this lane's token.  The anchor's coefficient c = m f, f a power of two and
       // 1 <= |m| < 2: f goes into the constants, where powers of two are exact, and m multiplies the
@@ -1035,14 +1050,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
             uint4 kq[4];
             uint2 mq[4];
 #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (GS == 32) kq[j] = tb[16 * c + 4 * j];
+              if (NRES && pl == 0) mq[j] = cm[16 * c + 4 * j];
+            }
+#pragma unroll 1
             for (int hh = 0; hh < 2; ++hh) {
-              if (hh == 0 || GS == 16) {
+              if (GS == 16) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) kq[j] = tb[(GS == 16 ? hh * 32 : 0) + 16 * c + 4 * j];
-              }
-              if (NRES && pl == 0 && hh == 0) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mq[j] = cm[16 * c + 4 * j];
+                for (int j = 0; j < 4; ++j) kq[j] = tb[hh * 32 + 16 * c + 4 * j];
               }
               uint32_t r[16];
 #pragma unroll
@@ -1084,7 +1100,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         if (lane == 0) mbar_arrive(&vfull_bar[pl]);
       }
       if (lane == 0) mbar_arrive(&empty_bar[st]);
-      if (it + 1 < n_it) cur.next(rows_s, per);
+      if (++st == ST) { st = 0; par ^= 1; }
     }
   }
   tc_before();
