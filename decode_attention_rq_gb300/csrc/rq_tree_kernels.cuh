@@ -14,8 +14,9 @@
 //   values  O^T [channels x NB] += V'^T P^T     (anchor and residual part apart)
 // K' and V'^T are dequantized into registers and stored to tensor memory as the A operand
 // (f16, one token or channel per lane): dequantized data never touches shared memory.
-// Roles (14 warps): K dequantizer, softmax, V dequantizer (4 warps each, one per 32
-// lanes), one copy warp, one MMA warp.
+// Roles (20 warps, in groups of four, one per 32 lanes): K, softmax, V of the anchor, V of the
+// residual (anchor loop: the other half of the anchor's), and a group with the copy warp and
+// one warp for each kind of product.
 //
 // Dequantization: an f16 whose bits are an integer n < 1024 has the value n 2^-24, so masking a
 // code word leaves codes times 2^(p - 24), p the field's first bit; one fused multiply-add with
@@ -63,7 +64,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTreeStep = 128;               // tokens per step: two layout tiles
-constexpr int kTreeThreads = 14 * 32;
+constexpr int kTreeThreads = 20 * 32;
 constexpr int kTreeRows = RQ_MAX_DECODE_BATCH;
 constexpr int kMergeQ = 8;                   // queries per merge CTA
 constexpr int kPrepQ = 8;                    // queries per prep CTA
@@ -121,6 +122,18 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
+template <int N>
+__device__ __forceinline__ void tc_chain(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t b_step, uint32_t idesc,
+                                         bool fresh) {
+  const uint64_t b0 = (uint64_t)b_hi << 32 | b_lo;
+  if (fresh) tc_mma<false>(d, a, b0, idesc); else tc_mma<true>(d, a, b0, idesc);
+#pragma unroll 1
+  for (int k = 1; k < N; ++k) {
+    a += 8;
+    b_lo += b_step;
+    tc_mma<true>(d, a, (uint64_t)b_hi << 32 | b_lo, idesc);
+  }
+}
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -152,13 +165,14 @@ __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
 constexpr uint32_t tc_idesc(int n, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n / 8) << 17) | ((128u / 16) << 24);
 }
-// Shared-memory operand in 128-byte rows, 8-row groups 1024 bytes apart, 128-byte swizzle
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(1024 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 |
-         2ull << 61;
-}
+// Shared-memory operands.  Queries: 16 channels of a row make 32 bytes, 8 rows 256 (32-byte
+// swizzle), so that the products of a plane step through blocks of NB * 32 bytes.  Weights: a
+// token's 64 queries make 128 bytes, 8 tokens 1024 (128-byte swizzle).
+constexpr uint32_t kDescHiQ = (256u >> 4) | 1u << 14 | 6u << 29, kDescHiP = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr & 0x3FFFF) >> 4 | (1024u >> 4) << 16; }
 // Named barrier of one warpgroup; wg_any: true when any thread's predicate holds.
 __device__ __forceinline__ void wg_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void wg_sync2(int id) { asm volatile("barrier.cta.sync %0, 256;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool wg_any(int id, bool p) {
   uint32_t r;
   asm volatile(
@@ -169,6 +183,8 @@ __device__ __forceinline__ bool wg_any(int id, bool p) {
       : "memory");
   return r != 0;
 }
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -315,19 +331,23 @@ struct TreeCfg {
   static constexpr int AV = 2 * A_TILE, RK = 4 * A_TILE, RV = 4 * A_TILE + 2 * R_TILE;
   static constexpr int STAGE = 4 * A_TILE + NRES * 4 * R_TILE;
   static constexpr int PL = 1 + NRES;
-  static constexpr int QBLK = NB * 128;                    // 64 channels of all queries
-  static constexpr int IMG = PL * 2 * QBLK;                // query operand of a unit
+  static constexpr int QSTEP = NB * 32;                    // 16 channels of all queries
+  static constexpr int IMG = PL * (D / 16) * QSTEP;        // query operand of a unit
   static constexpr int PBUF = kTreeStep * 128;             // weights: 128-byte row per token
   static constexpr int TAB = PL * NG * 64 * 8 + NRES * 256; // V constants
-  static constexpr int FIX = 2 * IMG + 2 * PBUF + TAB;
+  static constexpr int FIX = 2 * IMG + PBUF + TAB;
   static constexpr int STAGES = FIX + 4 * STAGE + 6144 <= 226 * 1024 ? 4 : 3;
   static constexpr int SMEM = FIX + STAGES * STAGE + 1024;
-  static constexpr int SBUF = NB <= 32 ? 2 : 1;
   // tensor memory columns
   static constexpr int KA = 0, KR = 64, VA = 128, VR = 192, OA = 256, OR = 256 + NB, S0 = 256 + 2 * NB;
   static constexpr int SCOLS = 2 * NB;                     // Sa, Sr
-  static_assert(S0 + SBUF * SCOLS <= 512, "tensor memory");
+  static_assert(S0 + SCOLS <= 512, "tensor memory");
   static_assert(SMEM <= 227 * 1024 - 5120, "shared memory");
+  // registers a thread: 96 at launch (5 groups: 480), then softmax, the three dequantizers, copies
+  static constexpr int REGS = NB == 64 ? 176 : 136;
+  static constexpr int REGD = NB == 64 ? 80 : 96;
+  static constexpr int REGP = 56;
+  static_assert(REGS + 3 * REGD + REGP <= 480, "registers");
   // floats of a partial: m[NB], l[NB], O as [plane][NB/4][D][4]
   static constexpr int PSTRIDE = 2 * NB + PL * NB * D;
 };
@@ -340,7 +360,7 @@ template <int D, int NRES, int NB>
 __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
   constexpr int RPW = D / 8;
   constexpr int PL = 1 + NRES;
-  constexpr int IMG = PL * 2 * NB * 128;
+  constexpr int IMG = PL * (D / 16) * NB * 32;
   __shared__ __align__(16) float q_s[kPrepQ][128];
   __shared__ float r_s[kPrepQ][128];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -432,8 +452,8 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
       const int lo = k_channel<D>(4 * c + j, pl != 0);
       w[j] = f16x2(x[lo], x[lo + (pl ? 8 : 4)]);
     }
-    const int r = q0 + qi, kb = c >> 3, chunk = c & 7;
-    *reinterpret_cast<uint4*>(img + (pl * 2 + kb) * (NB * 128) + r * 128 + ((chunk ^ (r & 7)) << 4)) =
+    const int r = q0 + qi;
+    *reinterpret_cast<uint4*>(img + ((pl * (D / 16) + (c >> 1)) * NB + r) * 32 + (((c & 1) ^ ((r >> 2) & 1)) << 4)) =
         make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
@@ -442,10 +462,10 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
 template <int D, int GS, int NRES, int NB>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
   using C = TreeCfg<D, GS, NRES, NB>;
-  constexpr int ST = C::STAGES, NG = C::NG, PL = C::PL, SB = C::SBUF;
+  constexpr int ST = C::STAGES, NG = C::NG, PL = C::PL;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full_bar[ST], empty_bar[ST], qfull_bar[2], qempty_bar[2], kfull_bar[2], kempty_bar[2],
-      vfull_bar[2], vempty_bar[2], sfull_bar[2], sempty_bar[2], pfull_bar[2], pempty_bar[2], drain_bar;
+      vfull_bar[2], vempty_bar[2], sfull_bar, sempty_bar, pfull_bar, pempty_bar, drain_bar[2];
   __shared__ TreeRowsShared rows_s;
   __shared__ __align__(16) float qm_s[NB / 2][4];   // two queries: their scales, minus their references
   __shared__ __align__(16) float f_s[NB];
@@ -457,8 +477,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
   // aligned by an offset, not by a cast: the compiler keeps the address space (shared, not generic, loads)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* q_img = smem;                                  // two query operands
-  uint8_t* p_buf = q_img + 2 * C::IMG;                    // two weight buffers
-  uint8_t* stages = p_buf + 2 * C::PBUF;
+  uint8_t* p_buf = q_img + 2 * C::IMG;                    // weights
+  uint8_t* stages = p_buf + C::PBUF;
   uint8_t* tab = stages + ST * C::STAGE;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -466,15 +486,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
 
   tree_rows(a, &rows_s);
   if (tid == 32) {
-    for (int i = 0; i < ST; ++i) { mbar_init(&full_bar[i], 1); mbar_init(&empty_bar[i], NRES ? 12 : 8); }
+    for (int i = 0; i < ST; ++i) { mbar_init(&full_bar[i], 1); mbar_init(&empty_bar[i], NRES ? 16 : 12); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull_bar[i], 1); mbar_init(&qempty_bar[i], 1);
       mbar_init(&kfull_bar[i], 4); mbar_init(&kempty_bar[i], 1);
-      mbar_init(&vfull_bar[i], 4); mbar_init(&vempty_bar[i], 1);
-      mbar_init(&sfull_bar[i], 1); mbar_init(&sempty_bar[i], 4);
-      mbar_init(&pfull_bar[i], 4); mbar_init(&pempty_bar[i], 1);
+      mbar_init(&vfull_bar[i], NRES ? 4 : 8); mbar_init(&vempty_bar[i], 1);
     }
-    mbar_init(&drain_bar, 1);
+    mbar_init(&sfull_bar, 1); mbar_init(&sempty_bar, 4);
+    mbar_init(&pfull_bar, 4); mbar_init(&pempty_bar, 1);
+    mbar_init(&drain_bar[0], 1); mbar_init(&drain_bar[1], 1);
     fence_mbar_init();
   }
   __syncthreads();
@@ -486,7 +506,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     pdl_wait();
     return;
   }
-  if (warp == 13) {
+  if (warp == 17) {
     tc_alloc(&tmem_s, 512);
     tc_relinquish();
     tc_before();
@@ -511,7 +531,133 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     (void)wait(bar, parity);
     __syncwarp();
   };
-  if (warp == 12) {
+  // ================= V: rows of channels, plane pl =================
+  auto v_role = [&](auto plane, int part) {
+    constexpr int pl = decltype(plane)::value;
+    const int w4 = warp & 3, lt = tid & 127;
+    auto v_sync = [&]() { if (NRES) wg_sync(2 + pl); else wg_sync2(2); };   // the groups that share constants
+    const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
+    const int col = v_slot(lt) >> 1, hf = v_slot(lt) & 1;   // the token's place among the constants
+    const int t4 = lane & 3;                                // the lane's 32 tokens: 32 t4 ..
+    const int tok = lt & 63, tau = lt >> 6;
+    // the field of this token in residual words starts at bit 2, 2, 4, 6 (as codes2 leaves it); its
+    // multiplier is that many powers of two below the one of bit 4
+    const int quad = (lt & 31) >> 2;
+    const __half2 field = __halves2half2(half_pow2((quad & 3) < 2 ? 2 : ((quad & 3) == 2 ? 0 : -2)), half_pow2(0));
+    const __half2 to_k = __halves2half2(half_pow2(24 - 4 - kScaleK), __ushort_as_half(0x0200));     // 2^5, 2^-15
+    int st = 0;
+    uint32_t par = 0;
+#pragma unroll 1
+    for (int it = 0; it < n_it; ++it) {
+      wait_warp(&full_bar[st], par);
+      const uint8_t* s = stages + st * C::STAGE;
+      const bool on = lt < (info_s[it & 7].x & 255);
+      v_sync();   // the previous step's constants are used up
+      // Constants of this lane's token.  The anchor's coefficient c = m f, f a power of two and
+      // 1 <= |m| < 2: f goes into the constants, where powers of two are exact, and m multiplies the
+      // finished f (s code + o), so that a value is rounded relative to itself and not to its group's
+      // range.  That product carries 2^-7: its operands 2^-13 and m 2^6.
+      __half2 f1 = __half2half2(half_pow2(0)), f2 = f1;
+      if (NRES && pl == 0) {
+        uint16_t cb =
+            *reinterpret_cast<const uint16_t*>(s + C::RV + tau * C::R_TILE + C::R_CODES + C::META + tok * 2);
+        if ((cb & 0x7F80) == 0 || !on) cb = 0;                          // a subnormal c counts as zero
+        const int e = (cb >> 7) & 0xFF;
+        // 4 f = 2^(e - 125) as two factors of f16 range; infinite and NaN c keep f = 1
+        const int x = (e == 0 || e == 255 ? 0 : e - 127) + 2, x1 = min(max(x, -14), 15), x2 = min(max(x - x1, -14), 15);
+        f1 = __half2half2(half_pow2(x1));
+        f2 = __half2half2(half_pow2(x2));
+        const uint32_t m = e == 255 || e == 0 ? cb : (cb & 0x807Fu) | 0x3F80u;   // c's sign and significand
+        *reinterpret_cast<__half*>(tab + PL * NG * 512 + col * 4 + hf * 2) =
+            __float2half_rn(bf16_bits_to_f32(m) * 64.f);
+      }
+      {
+        const uint8_t* tile = pl ? s + C::RV + tau * C::R_TILE : s + C::AV + tau * C::A_TILE;
+        const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + (pl ? C::R_CODES : C::A_CODES)) + tok * NG;
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+          if (!NRES && (gi & 1) != part) continue;
+          __half2 so = __hmul2(e4m3_pair(on ? meta[gi] : (uint16_t)0), to_k);
+          if (pl) so = __hmul2(so, field);
+          else if (NRES) so = __hmul2(__hmul2(so, f1), f2);
+          uint8_t* e = tab + ((pl * NG + gi) * 64 + col) * 8 + hf * 2;
+          *reinterpret_cast<__half*>(e) = __low2half(so);
+          *reinterpret_cast<__half*>(e + 4) = __high2half(so);
+        }
+      }
+      v_sync();
+      {
+        wait_warp(&vempty_bar[pl], (it & 1) ^ 1);
+        tc_after();
+        if (D == 128 || w4 < 3) {
+          // four lanes share a channel, 32 tokens each; a lane has four channels (l / 4 + 8 k), so that
+          // a constant read from shared memory serves four (groups of 16 channels: two)
+          const uint8_t* row = (pl ? s + C::RV + (t4 >> 1) * C::R_TILE : s + C::AV + (t4 >> 1) * C::A_TILE) +
+                               (w4 * 32 + (lane >> 2)) * (pl ? 16 : 32) + (t4 & 1) * (pl ? 8 : 16);
+          const uint4* tb = reinterpret_cast<const uint4*>(tab + (pl * NG + w4 * (32 / GS)) * 512) + t4;
+          const uint2* cm = reinterpret_cast<const uint2*>(tab + PL * NG * 512) + t4;   // significands of c
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {        // 16 of the lane's tokens: four pairs of columns
+            uint4 kq[4];
+            uint2 mq[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (GS == 32) kq[j] = tb[16 * c + 4 * j];
+              if (NRES && pl == 0) mq[j] = cm[16 * c + 4 * j];
+            }
+#pragma unroll 1
+            for (int hh = NRES ? 0 : part; hh < (NRES ? 2 : part + 1); ++hh) {
+              if (GS == 16) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) kq[j] = tb[hh * 32 + 16 * c + 4 * j];
+              }
+              uint32_t r[16];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint8_t* p = row + (16 * hh + 8 * k) * (pl ? 16 : 32) + c * (pl ? 4 : 8);
+                if (pl == 0) {
+                  const uint2 w = *reinterpret_cast<const uint2*>(p);
+                  const uint32_t ww[2] = {w.x, w.y};
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    uint32_t v[4];
+                    codes4(ww[i], v);          // v[x]: tokens (0, 2) of quad x & 1 from token x >> 1
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                      const int j = 2 * i + (x & 1), e = x >> 1;
+                      __half2 z = __hfma2(u2h(v[x]), u2h(e ? kq[j].z : kq[j].x), u2h(e ? kq[j].w : kq[j].y));
+                      if (NRES) z = __hmul2(z, u2h(e ? mq[j].y : mq[j].x));
+                      r[4 * j + 2 * k + e] = h2u(z);
+                    }
+                  }
+                } else {
+                  uint32_t v[8];
+                  codes2(*reinterpret_cast<const uint32_t*>(p), v);   // v[4 e + j]: quad j from token e
+#pragma unroll
+                  for (int x = 0; x < 8; ++x) {
+                    const int j = x & 3, e = x >> 2;
+                    r[4 * j + 2 * k + e] =
+                        h2u(__hfma2(u2h(v[x]), u2h(e ? kq[j].z : kq[j].x), u2h(e ? kq[j].w : kq[j].y)));
+                  }
+                }
+              }
+              tc_st_frag(lanes + ((uint32_t)(16 * hh) << 16) + (pl ? C::VR : C::VA) + 32 * c, r);
+            }
+          }
+          tc_wait_st();
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&vfull_bar[pl]);
+      }
+      if (lane == 0) mbar_arrive(&empty_bar[st]);
+      if (++st == ST) { st = 0; par ^= 1; }
+    }
+  };
+
+  if (warp >= 16) {
+    reg_dec<C::REGP>();
+  if (warp == 16) {
     // ================= copies =================
     if (lane == 0) {
       const uint64_t pol = l2_evict_first_policy();
@@ -581,79 +727,282 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       }
     }
     __syncwarp();
-  } else if (warp == 13) {
-    // ================= products =================
-    constexpr uint32_t id_s = tc_idesc(NB, false), id_o = tc_idesc(NB, true);
-    const uint64_t q_desc = tc_desc(smem_u32(q_img)), p_desc = tc_desc(smem_u32(p_buf));
+  } else if (warp == 17) {
+    // ================= products: scores =================
+    const uint32_t q_lo = desc_lo(smem_u32(q_img));
     int seg = -1;
-    bool first = false;
 #pragma unroll 1
-    for (int it = 0; it <= n_it; ++it) {   // S of step it, then O of the step before
-      const bool first_prev = first;
-      if (it < n_it) {
-        wait(&kfull_bar[0], it & 1);
-        const int flags = info_s[it & 7].x;
-        first = (flags & 256) != 0;
-        if (first) {
-          ++seg;
-          wait(&qfull_bar[seg & 1], (seg >> 1) & 1);
-        }
-        wait(&sempty_bar[it % SB], ((it / SB) & 1) ^ 1);
-#pragma unroll
-        for (int pl = 0; pl < PL; ++pl) {
-          if (pl) wait(&kfull_bar[pl], it & 1);
-          tc_after();
-          __syncwarp();
-          if (elect_one()) {
-            const uint32_t d = tmem + C::S0 + (it % SB) * C::SCOLS + pl * NB, k0 = tmem + (pl ? C::KR : C::KA);
-            uint64_t qd = q_desc + (((seg & 1) * C::IMG + pl * 2 * C::QBLK) >> 4);
-            tc_mma<false>(d, k0, qd, id_s);
-            tc_mma<true>(d, k0 + 8, qd + 2, id_s);
-#pragma unroll 1
-            for (int k = 2; k < D / 16; k += 2) {
-              qd += (k & 3) == 0 ? (C::QBLK >> 4) - 4 : 4;
-              tc_mma<true>(d, k0 + 8 * k, qd, id_s);
-              tc_mma<true>(d, k0 + 8 * k + 8, qd + 2, id_s);
-            }
-            tc_commit(&kempty_bar[pl]);
-            if (pl == PL - 1) {
-              tc_commit(&sfull_bar[it % SB]);
-              if (flags & 512) tc_commit(&qempty_bar[seg & 1]);
-            }
-          }
-          __syncwarp();
-        }
+    for (int it = 0; it < n_it; ++it) {
+      wait(&kfull_bar[0], it & 1);
+      const int flags = info_s[it & 7].x;
+      if (flags & 256) {
+        ++seg;
+        wait(&qfull_bar[seg & 1], (seg >> 1) & 1);
       }
-      if (it > 0) {   // O (+)= V' P of step it - 1
-        const int j = it - 1;
+      wait(&sempty_bar, (it & 1) ^ 1);
 #pragma unroll
-        for (int pl = 0; pl < PL; ++pl) {
-          wait(&vfull_bar[pl], j & 1);
-          if (pl == 0) wait(&pfull_bar[j & 1], (j >> 1) & 1);
-          tc_after();
-          __syncwarp();
-          if (elect_one()) {
-            const uint32_t o = tmem + (pl ? C::OR : C::OA), v = tmem + (pl ? C::VR : C::VA);
-            const uint64_t p0 = p_desc + (j & 1) * (C::PBUF >> 4);
-            if (first_prev) tc_mma<false>(o, v, p0, id_o); else tc_mma<true>(o, v, p0, id_o);
-            tc_mma<true>(o, v + 8, p0 + (2048 >> 4), id_o);
-#pragma unroll 1
-            for (int k = 2; k < kTreeStep / 16; k += 2) {
-              tc_mma<true>(o, v + 8 * k, p0 + k * (2048 >> 4), id_o);
-              tc_mma<true>(o, v + 8 * k + 8, p0 + (k + 1) * (2048 >> 4), id_o);
-            }
-            tc_commit(&vempty_bar[pl]);
-            if (pl == PL - 1) tc_commit(&pempty_bar[j & 1]);
+      for (int pl = 0; pl < PL; ++pl) {
+        if (pl) wait(&kfull_bar[pl], it & 1);
+        tc_after();
+        __syncwarp();
+        if (elect_one()) {
+          tc_chain<D / 16>(tmem + C::S0 + pl * NB, tmem + (pl ? C::KR : C::KA),
+                           q_lo + (((seg & 1) * C::IMG + pl * (D / 16) * C::QSTEP) >> 4), kDescHiQ, C::QSTEP >> 4,
+                           tc_idesc(NB, false), true);
+          tc_commit(&kempty_bar[pl]);
+          if (pl == PL - 1) {
+            tc_commit(&sfull_bar);
+            if (flags & 512) tc_commit(&qempty_bar[seg & 1]);
           }
-          __syncwarp();
         }
+        __syncwarp();
       }
     }
     // every product has ended before tensor memory is given back
-    if (elect_one()) tc_commit(&drain_bar);
-    wait(&drain_bar, 0);
+    if (elect_one()) tc_commit(&drain_bar[0]);
+    wait(&drain_bar[0], 0);
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp == 18) {
+    // ================= products: values =================
+    const uint32_t p_lo = desc_lo(smem_u32(p_buf));
+#pragma unroll 1
+    for (int it = 0; it < n_it; ++it) {
+#pragma unroll
+      for (int pl = 0; pl < PL; ++pl) {
+        wait(&vfull_bar[pl], it & 1);
+        if (pl == 0) wait(&pfull_bar, it & 1);
+        tc_after();
+        __syncwarp();
+        const bool first = (info_s[it & 7].x & 256) != 0;
+        if (elect_one()) {
+          tc_chain<kTreeStep / 16>(tmem + (pl ? C::OR : C::OA), tmem + (pl ? C::VR : C::VA), p_lo, kDescHiP, 2048 >> 4,
+                                   tc_idesc(NB, true), first);
+          tc_commit(&vempty_bar[pl]);
+          if (pl == PL - 1) tc_commit(&pempty_bar);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) tc_commit(&drain_bar[1]);
+    wait(&drain_bar[1], 0);
+    __syncwarp();
+  }
+  } else if (warp >= 4 && warp < 8) {
+    reg_inc<C::REGS>();
+    // ================= softmax: one token a lane =================
+    const int lt = tid - 128, tok = lt & 63, tau = lt >> 6, w4 = warp - 4;
+    const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
+    const int slot = v_slot(lt);
+    constexpr bool KEEP = NB <= 32;
+    float l[NB];
+    pdl_wait();
+    int st = 0;
+    uint32_t par = 0;
+#pragma unroll 1
+    for (int it = 0; it < n_it; ++it) {
+      if (NRES) wait_warp(&full_bar[st], par); else wait_warp(&sfull_bar, it & 1);
+      const int2 info = info_s[it & 7];
+      const bool first = (info.x & 256) != 0, on = lt < (info.x & 255);
+      const int unit = info.y;
+      if (first) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) l[i] = 0.f;
+        if (lt < NB) {
+          qm_s[lt >> 1][lt & 1] = __ldcg(a.q_scale + (size_t)unit * NB + lt);
+          qm_s[lt >> 1][2 + (lt & 1)] = INFINITY;
+        }
+        wg_sync(1);
+      }
+      float c = 0.f;
+      if (NRES) {
+        const uint16_t cb = *reinterpret_cast<const uint16_t*>(stages + st * C::STAGE + C::RK + tau * C::R_TILE +
+                                                               C::R_CODES + C::META + tok * 2);
+        c = on ? bf16_bits_to_f32(cb) : 0.f;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty_bar[st]);
+        if (++st == ST) { st = 0; par ^= 1; }
+        wait_warp(&sfull_bar, it & 1);
+      }
+      const float2 c2 = make_float2(c, c);
+      tc_after();
+      const uint32_t s0 = lanes + C::S0;
+      // score products of 16 queries with this lane's token
+      auto scores = [&](int ch, float2 (&y)[8]) {
+        uint32_t ra[16], rr[16];
+        tc_ld16(s0 + 16 * ch, ra);
+        if (NRES) tc_ld16(s0 + NB + 16 * ch, rr);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          y[i] = make_float2(__uint_as_float(ra[2 * i]), __uint_as_float(ra[2 * i + 1]));
+          if (NRES)
+            y[i] = fma2(y[i], c2, make_float2(__uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1])));
+        }
+      };
+      // ... in log2 units, relative to the query's reference
+      auto relative = [&](int ch, float2 (&y)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 k = *reinterpret_cast<const float4*>(qm_s[8 * ch + i]);
+          y[i] = fma2(y[i], make_float2(k.x, k.y), make_float2(k.z, k.w));
+        }
+      };
+      float top = -INFINITY;
+      float2 kept[KEEP ? NB / 2 : 1];     // relative scores, where they fit the registers
+#pragma unroll
+      for (int ch = 0; ch < NB / 16; ++ch) {
+        float2 y[8];
+        scores(ch, y);
+        relative(ch, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          top = fmaxf(top, fmaxf(y[i].x, y[i].y));
+          if (KEEP) kept[(KEEP ? 8 * ch + i : 0)] = y[i];
+        }
+      }
+      if (__builtin_expect(wg_any(1, on && top > kTop), 0)) {
+        // move the references to this step's maxima where those are higher
+#pragma unroll
+        for (int ch = 0; ch < NB / 16; ++ch) {
+          float2 y[8];
+          scores(ch, y);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float v = on ? (i & 1 ? y[i / 2].y : y[i / 2].x) * qm_s[8 * ch + i / 2][i & 1] : -INFINITY;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            if (lane == 0) wred_s[w4][16 * ch + i] = v;
+          }
+        }
+        wg_sync(1);
+        if (lt < NB) {
+          const float old = -qm_s[lt >> 1][2 + (lt & 1)];
+          const float mx = fmaxf(fmaxf(wred_s[0][lt], wred_s[1][lt]), fmaxf(wred_s[2][lt], wred_s[3][lt])) - kHead;
+          const float now = fmaxf(old, mx);
+          f_s[lt] = old == now ? 1.f : exp2f(old - now);
+          qm_s[lt >> 1][2 + (lt & 1)] = -now;
+        }
+        wg_sync(1);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) l[i] *= f_s[i];
+        if (!first) {   // O holds products of the steps before: all of them done, then scaled
+          wait_warp(&pempty_bar, (it - 1) & 1);
+          tc_after();
+#pragma unroll
+          for (int ch = 0; ch < PL * NB / 16; ++ch) {
+            uint32_t r[16];
+            tc_ld16(lanes + C::OA + 16 * ch, r);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f_s[(16 * ch + i) % NB]);
+            tc_st16(lanes + C::OA + 16 * ch, r);
+          }
+          tc_wait_st();
+        }
+        if (KEEP) {
+#pragma unroll
+          for (int ch = 0; ch < NB / 16; ++ch) {
+            float2 y[8];
+            scores(ch, y);
+            relative(ch, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) kept[(KEEP ? 8 * ch + i : 0)] = y[i];
+          }
+        }
+      }
+      // weights
+      if (KEEP) {   // the scores are in registers: their place in tensor memory is free
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty_bar);
+      }
+      wait_warp(&pempty_bar, (it & 1) ^ 1);
+      uint8_t* prow = p_buf + slot * 128;
+#pragma unroll
+      for (int ch = 0; ch < NB / 16; ++ch) {
+        float2 y[8];
+        if (KEEP) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = kept[(KEEP ? 8 * ch + i : 0)];
+        } else {
+          scores(ch, y);
+          relative(ch, y);
+        }
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          y[i].x = on ? ex2_fast(y[i].x) : 0.f;
+          y[i].y = on ? ex2_fast(y[i].y) : 0.f;
+          l[16 * ch + 2 * i] += y[i].x;
+          l[16 * ch + 2 * i + 1] += y[i].y;
+          w[i] = f16x2(y[i].x, y[i].y);
+        }
+        *reinterpret_cast<uint4*>(prow + (((2 * ch) ^ (slot & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(prow + (((2 * ch + 1) ^ (slot & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+      fence_async_smem();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (!KEEP) mbar_arrive(&sempty_bar);
+        mbar_arrive(&pfull_bar);
+      }
+      if (__builtin_expect((info.x & 512) != 0, 0)) {
+        // the unit's state out
+        wait_warp(&pempty_bar, it & 1);
+        tc_after();
+        float* part = a.partials + (size_t)(blockIdx.x + unit) * a.pstride;
+        if (lt < D) {
+#pragma unroll
+          for (int c = 0; c < PL * NB / 16; ++c) {
+            uint32_t r[16];
+            if (D == 128 || w4 < 3) {
+              tc_ld16(lanes + C::OA + 16 * c, r);
+              tc_wait_ld();
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(part + 2 * NB + ((size_t)(4 * c + i) * D + lt) * 4) =
+                  make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+          }
+        }
+        tc_before();
+        // sums over the lanes: reduce-scatter, then over the warps in order
+#pragma unroll
+        for (int o = 16, n = NB / 2; o >= 1; o >>= 1) {
+          if (n >= 1) {
+            const bool up = (lane & o) != 0;
+#pragma unroll
+            for (int i = 0; i < (NB >= 32 ? NB / 2 : 8); ++i)
+              if (i < n) {
+                const float send = up ? l[i] : l[i + n], keep = up ? l[i + n] : l[i];
+                l[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+              }
+            n >>= 1;
+          } else {
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+          }
+        }
+        // NB = 64: lane holds queries q0, q0 + 1 ...: the bits of the lane, highest first
+        if (NB == 64) {
+          wred_s[w4][lane * 2] = l[0];
+          wred_s[w4][lane * 2 + 1] = l[1];
+        } else if (NB == 32) {
+          wred_s[w4][lane] = l[0];
+        } else if ((lane & 1) == 0) {
+          wred_s[w4][lane >> 1] = l[0];
+        }
+        wg_sync(1);
+        if (lt < NB) {
+          part[lt] = -qm_s[lt >> 1][2 + (lt & 1)];
+          part[NB + lt] = wred_s[0][lt] + wred_s[1][lt] + wred_s[2][lt] + wred_s[3][lt];
+        }
+        wg_sync(1);
+      }
+    }
+  } else {
+    if (C::REGD < 96) reg_dec<C::REGD>();
+    if (warp < 4) {
     // ================= K: rows of tokens =================
     const int tau = warp >> 1;                              // the warp's tile of the step
     const int t4 = lane & 3, base = warp * 32;
@@ -774,338 +1123,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       if (lane == 0) mbar_arrive(&empty_bar[st]);
       if (++st == ST) { st = 0; par ^= 1; }
     }
-  } else if (warp < 8) {
-    // ================= softmax: one token a lane =================
-    const int lt = tid - 128, tok = lt & 63, tau = lt >> 6, w4 = warp - 4;
-    const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
-    const int slot = v_slot(lt);
-    constexpr bool KEEP = NB <= 32;
-    float l[NB];
-    pdl_wait();
-    int st = 0;
-    uint32_t par = 0;
-#pragma unroll 1
-    for (int it = 0; it < n_it; ++it) {
-      if (NRES) wait_warp(&full_bar[st], par); else wait_warp(&sfull_bar[it % SB], (it / SB) & 1);
-      const int2 info = info_s[it & 7];
-      const bool first = (info.x & 256) != 0, on = lt < (info.x & 255);
-      const int unit = info.y;
-      if (first) {
-#pragma unroll
-        for (int i = 0; i < NB; ++i) l[i] = 0.f;
-        if (lt < NB) {
-          qm_s[lt >> 1][lt & 1] = __ldcg(a.q_scale + (size_t)unit * NB + lt);
-          qm_s[lt >> 1][2 + (lt & 1)] = INFINITY;
-        }
-        wg_sync(1);
-      }
-      float c = 0.f;
-      if (NRES) {
-        const uint16_t cb = *reinterpret_cast<const uint16_t*>(stages + st * C::STAGE + C::RK + tau * C::R_TILE +
-                                                               C::R_CODES + C::META + tok * 2);
-        c = on ? bf16_bits_to_f32(cb) : 0.f;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty_bar[st]);
-        if (++st == ST) { st = 0; par ^= 1; }
-        wait_warp(&sfull_bar[it % SB], (it / SB) & 1);
-      }
-      const float2 c2 = make_float2(c, c);
-      tc_after();
-      const uint32_t s0 = lanes + C::S0 + (it % SB) * C::SCOLS;
-      // score products of 16 queries with this lane's token
-      auto scores = [&](int ch, float2 (&y)[8]) {
-        uint32_t ra[16], rr[16];
-        tc_ld16(s0 + 16 * ch, ra);
-        if (NRES) tc_ld16(s0 + NB + 16 * ch, rr);
-        tc_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[i] = make_float2(__uint_as_float(ra[2 * i]), __uint_as_float(ra[2 * i + 1]));
-          if (NRES)
-            y[i] = fma2(y[i], c2, make_float2(__uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1])));
-        }
-      };
-      // ... in log2 units, relative to the query's reference
-      auto relative = [&](int ch, float2 (&y)[8]) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 k = *reinterpret_cast<const float4*>(qm_s[8 * ch + i]);
-          y[i] = fma2(y[i], make_float2(k.x, k.y), make_float2(k.z, k.w));
-        }
-      };
-      float top = -INFINITY;
-      float2 kept[KEEP ? NB / 2 : 1];     // relative scores, where they fit the registers
-#pragma unroll
-      for (int ch = 0; ch < NB / 16; ++ch) {
-        float2 y[8];
-        scores(ch, y);
-        relative(ch, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          top = fmaxf(top, fmaxf(y[i].x, y[i].y));
-          if (KEEP) kept[(KEEP ? 8 * ch + i : 0)] = y[i];
-        }
-      }
-      if (__builtin_expect(wg_any(1, on && top > kTop), 0)) {
-        // move the references to this step's maxima where those are higher
-#pragma unroll
-        for (int ch = 0; ch < NB / 16; ++ch) {
-          float2 y[8];
-          scores(ch, y);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float v = on ? (i & 1 ? y[i / 2].y : y[i / 2].x) * qm_s[8 * ch + i / 2][i & 1] : -INFINITY;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-            if (lane == 0) wred_s[w4][16 * ch + i] = v;
-          }
-        }
-        wg_sync(1);
-        if (lt < NB) {
-          const float old = -qm_s[lt >> 1][2 + (lt & 1)];
-          const float mx = fmaxf(fmaxf(wred_s[0][lt], wred_s[1][lt]), fmaxf(wred_s[2][lt], wred_s[3][lt])) - kHead;
-          const float now = fmaxf(old, mx);
-          f_s[lt] = old == now ? 1.f : exp2f(old - now);
-          qm_s[lt >> 1][2 + (lt & 1)] = -now;
-        }
-        wg_sync(1);
-#pragma unroll
-        for (int i = 0; i < NB; ++i) l[i] *= f_s[i];
-        if (!first) {   // O holds products of the steps before: all of them done, then scaled
-          wait_warp(&pempty_bar[(it - 1) & 1], ((it - 1) >> 1) & 1);
-          tc_after();
-#pragma unroll
-          for (int ch = 0; ch < PL * NB / 16; ++ch) {
-            uint32_t r[16];
-            tc_ld16(lanes + C::OA + 16 * ch, r);
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f_s[(16 * ch + i) % NB]);
-            tc_st16(lanes + C::OA + 16 * ch, r);
-          }
-          tc_wait_st();
-        }
-        if (KEEP) {
-#pragma unroll
-          for (int ch = 0; ch < NB / 16; ++ch) {
-            float2 y[8];
-            scores(ch, y);
-            relative(ch, y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) kept[(KEEP ? 8 * ch + i : 0)] = y[i];
-          }
-        }
-      }
-      // weights
-      wait_warp(&pempty_bar[it & 1], ((it >> 1) & 1) ^ 1);
-      uint8_t* prow = p_buf + (it & 1) * C::PBUF + slot * 128;
-#pragma unroll
-      for (int ch = 0; ch < NB / 16; ++ch) {
-        float2 y[8];
-        if (KEEP) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = kept[(KEEP ? 8 * ch + i : 0)];
-        } else {
-          scores(ch, y);
-          relative(ch, y);
-        }
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[i].x = on ? ex2_fast(y[i].x) : 0.f;
-          y[i].y = on ? ex2_fast(y[i].y) : 0.f;
-          l[16 * ch + 2 * i] += y[i].x;
-          l[16 * ch + 2 * i + 1] += y[i].y;
-          w[i] = f16x2(y[i].x, y[i].y);
-        }
-        *reinterpret_cast<uint4*>(prow + (((2 * ch) ^ (slot & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(prow + (((2 * ch + 1) ^ (slot & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-      }
-      fence_async_smem();
-      tc_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sempty_bar[it % SB]);
-        mbar_arrive(&pfull_bar[it & 1]);
-      }
-      if (__builtin_expect((info.x & 512) != 0, 0)) {
-        // the unit's state out
-        wait_warp(&pempty_bar[it & 1], (it >> 1) & 1);
-        tc_after();
-        float* part = a.partials + (size_t)(blockIdx.x + unit) * a.pstride;
-        if (lt < D) {
-#pragma unroll
-          for (int c = 0; c < PL * NB / 16; ++c) {
-            uint32_t r[16];
-            if (D == 128 || w4 < 3) {
-              tc_ld16(lanes + C::OA + 16 * c, r);
-              tc_wait_ld();
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(part + 2 * NB + ((size_t)(4 * c + i) * D + lt) * 4) =
-                  make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-          }
-        }
-        tc_before();
-        // sums over the lanes: reduce-scatter, then over the warps in order
-#pragma unroll
-        for (int o = 16, n = NB / 2; o >= 1; o >>= 1) {
-          if (n >= 1) {
-            const bool up = (lane & o) != 0;
-#pragma unroll
-            for (int i = 0; i < (NB >= 32 ? NB / 2 : 8); ++i)
-              if (i < n) {
-                const float send = up ? l[i] : l[i + n], keep = up ? l[i + n] : l[i];
-                l[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-              }
-            n >>= 1;
-          } else {
-            l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
-          }
-        }
-        // NB = 64: lane holds queries q0, q0 + 1 ...: the bits of the lane, highest first
-        if (NB == 64) {
-          wred_s[w4][lane * 2] = l[0];
-          wred_s[w4][lane * 2 + 1] = l[1];
-        } else if (NB == 32) {
-          wred_s[w4][lane] = l[0];
-        } else if ((lane & 1) == 0) {
-          wred_s[w4][lane >> 1] = l[0];
-        }
-        wg_sync(1);
-        if (lt < NB) {
-          part[lt] = -qm_s[lt >> 1][2 + (lt & 1)];
-          part[NB + lt] = wred_s[0][lt] + wred_s[1][lt] + wred_s[2][lt] + wred_s[3][lt];
-        }
-        wg_sync(1);
-      }
-    }
-  } else {
-    // ================= V: rows of channels =================
-    const int lt = tid - 256, w4 = warp - 8;
-    const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
-    const int col = v_slot(lt) >> 1, hf = v_slot(lt) & 1;   // the token's place among the constants
-    const int t4 = lane & 3;                                // the lane's 32 tokens: 32 t4 ..
-    const int tok = lt & 63, tau = lt >> 6;
-    // the field of this token in residual words starts at bit 2, 2, 4, 6 (as codes2 leaves it); its
-    // multiplier is that many powers of two below the one of bit 4
-    const int quad = (lt & 31) >> 2;
-    const __half2 field = __halves2half2(half_pow2((quad & 3) < 2 ? 2 : ((quad & 3) == 2 ? 0 : -2)), half_pow2(0));
-    const __half2 to_k = __halves2half2(half_pow2(24 - 4 - kScaleK), __ushort_as_half(0x0200));     // 2^5, 2^-15
-    int st = 0;
-    uint32_t par = 0;
-#pragma unroll 1
-    for (int it = 0; it < n_it; ++it) {
-      wait_warp(&full_bar[st], par);
-      const uint8_t* s = stages + st * C::STAGE;
-      const bool on = lt < (info_s[it & 7].x & 255);
-      wg_sync(2);   // the previous step's constants are used up
-      // Constants of this lane's token.  The anchor's coefficient c = m f, f a power of two and
-      // 1 <= |m| < 2: f goes into the constants, where powers of two are exact, and m multiplies the
-      // finished f (s code + o), so that a value is rounded relative to itself and not to its group's
-      // range.  That product carries 2^-7: its operands 2^-13 and m 2^6.
-      __half2 f1 = __half2half2(half_pow2(0)), f2 = f1;
-      if (NRES) {
-        uint16_t cb =
-            *reinterpret_cast<const uint16_t*>(s + C::RV + tau * C::R_TILE + C::R_CODES + C::META + tok * 2);
-        if ((cb & 0x7F80) == 0 || !on) cb = 0;                          // a subnormal c counts as zero
-        const int e = (cb >> 7) & 0xFF;
-        // 4 f = 2^(e - 125) as two factors of f16 range; infinite and NaN c keep f = 1
-        const int x = (e == 0 || e == 255 ? 0 : e - 127) + 2, x1 = min(max(x, -14), 15), x2 = min(max(x - x1, -14), 15);
-        f1 = __half2half2(half_pow2(x1));
-        f2 = __half2half2(half_pow2(x2));
-        const uint32_t m = e == 255 || e == 0 ? cb : (cb & 0x807Fu) | 0x3F80u;   // c's sign and significand
-        *reinterpret_cast<__half*>(tab + PL * NG * 512 + col * 4 + hf * 2) =
-            __float2half_rn(bf16_bits_to_f32(m) * 64.f);
-      }
-#pragma unroll
-      for (int pl = 0; pl < PL; ++pl) {
-        const uint8_t* tile = pl ? s + C::RV + tau * C::R_TILE : s + C::AV + tau * C::A_TILE;
-        const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + (pl ? C::R_CODES : C::A_CODES)) + tok * NG;
-#pragma unroll
-        for (int gi = 0; gi < NG; ++gi) {
-          __half2 so = __hmul2(e4m3_pair(on ? meta[gi] : (uint16_t)0), to_k);
-          if (pl) so = __hmul2(so, field);
-          else if (NRES) so = __hmul2(__hmul2(so, f1), f2);
-          uint8_t* e = tab + ((pl * NG + gi) * 64 + col) * 8 + hf * 2;
-          *reinterpret_cast<__half*>(e) = __low2half(so);
-          *reinterpret_cast<__half*>(e + 4) = __high2half(so);
-        }
-      }
-      wg_sync(2);
-#pragma unroll
-      for (int pl = 0; pl < PL; ++pl) {
-        wait_warp(&vempty_bar[pl], (it & 1) ^ 1);
-        tc_after();
-        if (D == 128 || w4 < 3) {
-          // four lanes share a channel, 32 tokens each; a lane has four channels (l / 4 + 8 k), so that
-          // a constant read from shared memory serves four (groups of 16 channels: two)
-          const uint8_t* row = (pl ? s + C::RV + (t4 >> 1) * C::R_TILE : s + C::AV + (t4 >> 1) * C::A_TILE) +
-                               (w4 * 32 + (lane >> 2)) * (pl ? 16 : 32) + (t4 & 1) * (pl ? 8 : 16);
-          const uint4* tb = reinterpret_cast<const uint4*>(tab + (pl * NG + w4 * (32 / GS)) * 512) + t4;
-          const uint2* cm = reinterpret_cast<const uint2*>(tab + PL * NG * 512) + t4;   // significands of c
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {        // 16 of the lane's tokens: four pairs of columns
-            uint4 kq[4];
-            uint2 mq[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (GS == 32) kq[j] = tb[16 * c + 4 * j];
-              if (NRES && pl == 0) mq[j] = cm[16 * c + 4 * j];
-            }
-#pragma unroll 1
-            for (int hh = 0; hh < 2; ++hh) {
-              if (GS == 16) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) kq[j] = tb[hh * 32 + 16 * c + 4 * j];
-              }
-              uint32_t r[16];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint8_t* p = row + (16 * hh + 8 * k) * (pl ? 16 : 32) + c * (pl ? 4 : 8);
-                if (pl == 0) {
-                  const uint2 w = *reinterpret_cast<const uint2*>(p);
-                  const uint32_t ww[2] = {w.x, w.y};
-#pragma unroll
-                  for (int i = 0; i < 2; ++i) {
-                    uint32_t v[4];
-                    codes4(ww[i], v);          // v[x]: tokens (0, 2) of quad x & 1 from token x >> 1
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                      const int j = 2 * i + (x & 1), e = x >> 1;
-                      __half2 z = __hfma2(u2h(v[x]), u2h(e ? kq[j].z : kq[j].x), u2h(e ? kq[j].w : kq[j].y));
-                      if (NRES) z = __hmul2(z, u2h(e ? mq[j].y : mq[j].x));
-                      r[4 * j + 2 * k + e] = h2u(z);
-                    }
-                  }
-                } else {
-                  uint32_t v[8];
-                  codes2(*reinterpret_cast<const uint32_t*>(p), v);   // v[4 e + j]: quad j from token e
-#pragma unroll
-                  for (int x = 0; x < 8; ++x) {
-                    const int j = x & 3, e = x >> 2;
-                    r[4 * j + 2 * k + e] =
-                        h2u(__hfma2(u2h(v[x]), u2h(e ? kq[j].z : kq[j].x), u2h(e ? kq[j].w : kq[j].y)));
-                  }
-                }
-              }
-              tc_st_frag(lanes + ((uint32_t)(16 * hh) << 16) + (pl ? C::VR : C::VA) + 32 * c, r);
-            }
-          }
-          tc_wait_st();
-        }
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&vfull_bar[pl]);
-      }
-      if (lane == 0) mbar_arrive(&empty_bar[st]);
-      if (++st == ST) { st = 0; par ^= 1; }
+    } else if (warp < 12) {
+      v_role(std::integral_constant<int, 0>{}, 0);
+    } else {
+      v_role(std::integral_constant<int, NRES>{}, 1);
     }
   }
   tc_before();
   __syncthreads();
-  if (warp == 13) {
+  if (warp == 17) {
     tc_after();
     tc_dealloc(tmem, 512);
   }
