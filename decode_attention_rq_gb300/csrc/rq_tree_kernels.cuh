@@ -1138,27 +1138,44 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
 }
 
 // ---- merge -------------------------------------------------------------------------
-// One CTA per kMergeQ queries of a (row, KV head), thread = channel.  The drafted tokens
-// first (BF16 keys and values, float32 arithmetic; before the wait: nothing of it
-// depends on the streaming kernel), then the partial states, R^T, the quotient.
+// One CTA per kMergeQ queries of a (row, KV head).  The drafted tokens first (BF16 keys and
+// values through shared memory, float32 arithmetic; before the wait: nothing of it depends on
+// the streaming kernel), then the partial states, R^T, the quotient.  Two threads share a
+// channel (or a key): the loads of each part are all in flight at once, as the kernel is
+// nothing but a chain of latencies.
+constexpr int kMergeThreads = 256;
+constexpr int kDraftPitch = 272;       // bytes of a staged row: 16-byte reads of 8 rows hit 8 bank groups
+
 template <int D, int NRES, int NB>
-__global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, int ctas) {
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, int ctas) {
   __shared__ TreeRowsShared rows_s;
-  __shared__ __align__(16) float q_s[128][kMergeQ];          // [channel][query]
-  __shared__ __align__(16) float p_s[128][kMergeQ];          // [key][query], then R^T's operand [channel][query]
+  __shared__ __align__(16) uint8_t kv_s[128 * kDraftPitch];   // drafted keys, then values
+  __shared__ __align__(16) float q_s[128][kMergeQ];           // [channel][query]
+  __shared__ __align__(16) float p_s[128][kMergeQ];           // [key][query], then R^T's operand [channel][query]
+  __shared__ __align__(16) float h_s[128][kMergeQ];           // the upper half's share
   __shared__ unsigned long long vis_s[kMergeQ][RQ_MAX_TREE_NODES / 64];
   __shared__ float red_s[4][kMergeQ];
   __shared__ int range_s[2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = tid >> 7, ch = tid & 127;
   const int per_bh = (a.M + kMergeQ - 1) / kMergeQ;
   const int bh = blockIdx.x / per_bh, r0 = blockIdx.x % per_bh * kMergeQ, b = bh / a.g.H;
   const int nq = min(kMergeQ, a.M - r0);
-  tree_rows(a, &rows_s);
   const int cnt = a.counts ? clamp_len(a.counts[b], a.T) : a.T;
+  const uint4* kp = reinterpret_cast<const uint4*>(a.k_new + (size_t)bh * a.T * D);
+  const uint4* vp = reinterpret_cast<const uint4*>(a.v_new + (size_t)bh * a.T * D);
+  constexpr int RC = D / 8;              // 16-byte pieces of a row
+  // keys j0 .. of the draft into shared memory
+  auto stage = [&](const uint4* src, int j0) {
+    const int n = min(128, cnt - j0) * RC;
+#pragma unroll 4
+    for (int i = tid; i < n; i += kMergeThreads)
+      *reinterpret_cast<uint4*>(kv_s + (i / RC) * kDraftPitch + (i % RC) * 16) = __ldg(src + (size_t)j0 * RC + i);
+  };
   const __nv_bfloat16* qp = a.q + ((size_t)bh * a.M + r0) * D;
-  for (int i = tid; i < kMergeQ * D; i += 128) {
-    const int qi = i / D, ch = i % D;
-    q_s[ch][qi] = qi < nq ? __bfloat162float(qp[(size_t)qi * D + ch]) : 0.f;
+#pragma unroll
+  for (int i = tid; i < kMergeQ * D; i += kMergeThreads) {
+    const int qi = i / D, c = i % D;
+    q_s[c][qi] = qi < nq ? __bfloat162float(qp[(size_t)qi * D + c]) : 0.f;
   }
   if (tid < kMergeQ * (RQ_MAX_TREE_NODES / 64)) {
     const int qi = tid % kMergeQ, w = tid / kMergeQ, t = (r0 + qi) % a.T;
@@ -1170,38 +1187,68 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, int ctas) {
     }
     vis_s[qi][w] = v;
   }
+  if (cnt > 0) stage(kp, 0);
+  tree_rows(a, &rows_s);
   __syncthreads();
+  if (tid == 0) {   // the CTAs that hold a partial state of this unit
+    const int U = rows_s.pre[a.batch];
+    const int steps = (rows_s.len[b] + kTreeStep - 1) / kTreeStep;
+    range_s[0] = 0;
+    range_s[1] = -1;
+    if (steps) {
+      const TreeSplit split{U / ctas, U % ctas};
+      const int s0 = rows_s.pre[b] + (bh * a.nqb + r0 / NB - b * a.g.H * a.nqb) * steps;
+      range_s[0] = split.owner(s0);
+      range_s[1] = split.owner(s0 + steps - 1);
+    }
+  }
 
+  // m, l: of the whole draft, in every thread; o: this thread's channel, keys of its half
   float m[kMergeQ], l[kMergeQ], o[kMergeQ];
 #pragma unroll
   for (int i = 0; i < kMergeQ; ++i) { m[i] = -INFINITY; l[i] = 0.f; o[i] = 0.f; }
-  const __nv_bfloat16* kp = a.k_new + (size_t)bh * a.T * D;
-  const __nv_bfloat16* vp = a.v_new + (size_t)bh * a.T * D;
+#pragma unroll 1
   for (int j0 = 0; j0 < cnt; j0 += 128) {
-    const int j = j0 + tid;
+    const int nk = min(128, cnt - j0), key = tid & 127;   // key: this thread's, half of its channels
+    if (j0) {
+      __syncthreads();
+      stage(kp, j0);
+      __syncthreads();
+    }
     float s[kMergeQ];
 #pragma unroll
     for (int i = 0; i < kMergeQ; ++i) s[i] = 0.f;
-    if (j < cnt) {
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(kp + (size_t)j * D) + c);
+    if (key < nk) {
+#pragma unroll 2
+      for (int c = half * (RC / 2); c < (half + 1) * (RC / 2); ++c) {
+        const uint4 v = *reinterpret_cast<const uint4*>(kv_s + key * kDraftPitch + c * 16);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float k = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-#pragma unroll
-          for (int i = 0; i < kMergeQ; ++i) s[i] = fmaf(k, q_s[8 * c + e][i], s[i]);
+          const float4 x = *reinterpret_cast<const float4*>(q_s[8 * c + e]),
+                       y = *reinterpret_cast<const float4*>(q_s[8 * c + e] + 4);
+          s[0] = fmaf(k, x.x, s[0]); s[1] = fmaf(k, x.y, s[1]); s[2] = fmaf(k, x.z, s[2]); s[3] = fmaf(k, x.w, s[3]);
+          s[4] = fmaf(k, y.x, s[4]); s[5] = fmaf(k, y.y, s[5]); s[6] = fmaf(k, y.z, s[6]); s[7] = fmaf(k, y.w, s[7]);
         }
       }
     }
+    if (half) {
 #pragma unroll
-    for (int i = 0; i < kMergeQ; ++i) {
-      const bool on = j < cnt && ((vis_s[i][j >> 6] >> (j & 63)) & 1);
-      s[i] = on ? s[i] * a.qscale : -INFINITY;
-      float v = s[i];
+      for (int i = 0; i < kMergeQ; ++i) h_s[key][i] = s[i];
+    }
+    __syncthreads();
+    stage(vp, j0);     // the keys are used up
+    if (!half) {
 #pragma unroll
-      for (int f = 16; f > 0; f >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, f));
-      if (lane == 0) red_s[warp][i] = v;
+      for (int i = 0; i < kMergeQ; ++i) {
+        const bool on = key < nk && ((vis_s[i][(j0 + key) >> 6] >> ((j0 + key) & 63)) & 1);
+        s[i] = on ? (s[i] + h_s[key][i]) * a.qscale : -INFINITY;
+        float v = s[i];
+#pragma unroll
+        for (int f = 16; f > 0; f >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, f));
+        if (lane == 0) red_s[warp][i] = v;
+      }
     }
     __syncthreads();
 #pragma unroll
@@ -1212,115 +1259,124 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, int ctas) {
       l[i] *= f;
       o[i] *= f;
       m[i] = now;
-      const bool on = j < cnt && ((vis_s[i][j >> 6] >> (j & 63)) & 1);
-      s[i] = on ? exp2f(s[i] - ref) : 0.f;
-      p_s[tid][i] = s[i];
+      if (!half) {
+        const bool on = key < nk && ((vis_s[i][(j0 + key) >> 6] >> ((j0 + key) & 63)) & 1);
+        s[i] = on ? exp2f(s[i] - ref) : 0.f;   // a NaN score stays
+        p_s[key][i] = s[i];
+      }
     }
     __syncthreads();
+    if (!half) {
 #pragma unroll
-    for (int i = 0; i < kMergeQ; ++i) {
-      float v = s[i];
+      for (int i = 0; i < kMergeQ; ++i) {
+        float v = s[i];
 #pragma unroll
-      for (int f = 16; f > 0; f >>= 1) v += __shfl_xor_sync(0xffffffffu, v, f);
-      if (lane == 0) red_s[warp][i] = v;
+        for (int f = 16; f > 0; f >>= 1) v += __shfl_xor_sync(0xffffffffu, v, f);
+        if (lane == 0) red_s[warp][i] = v;
+      }
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMergeQ; ++i) l[i] += (red_s[0][i] + red_s[1][i]) + (red_s[2][i] + red_s[3][i]);
-    if (tid < D) {
-      const int nk = min(128, cnt - j0);
-      for (int k = 0; k < nk; ++k) {
-        const float v = __bfloat162float(vp[(size_t)(j0 + k) * D + tid]);
+    if (ch < D) {
+      for (int k = half; k < nk; k += 2) {
+        const float v = bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(kv_s + k * kDraftPitch + ch * 2));
+        const float4 x = *reinterpret_cast<const float4*>(p_s[k]), y = *reinterpret_cast<const float4*>(p_s[k] + 4);
+        const float pk[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         if (isfinite(v)) {
 #pragma unroll
-          for (int i = 0; i < kMergeQ; ++i) o[i] = fmaf(p_s[k][i], v, o[i]);
+          for (int i = 0; i < kMergeQ; ++i) o[i] = fmaf(pk[i], v, o[i]);
         } else {   // enters only where it is seen
 #pragma unroll
           for (int i = 0; i < kMergeQ; ++i)
-            if ((vis_s[i][(j0 + k) >> 6] >> ((j0 + k) & 63)) & 1) o[i] = fmaf(p_s[k][i], v, o[i]);
+            if ((vis_s[i][(j0 + k) >> 6] >> ((j0 + k) & 63)) & 1) o[i] = fmaf(pk[i], v, o[i]);
         }
       }
     }
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMergeQ; ++i) l[i] += (red_s[0][i] + red_s[1][i]) + (red_s[2][i] + red_s[3][i]);
   }
 
-  // the cached tokens' partial states
-  if (tid == 0) {
-    const int U = rows_s.pre[a.batch];
-    const int steps = (rows_s.len[b] + kTreeStep - 1) / kTreeStep;
-    range_s[0] = 0;
-    range_s[1] = -1;
-    if (steps) {
-      const TreeSplit split{U / ctas, U % ctas};
-      const int unit = bh * a.nqb + r0 / NB;
-      const int s0 = rows_s.pre[b] + (unit - b * a.g.H * a.nqb) * steps;
-      range_s[0] = split.owner(s0);
-      range_s[1] = split.owner(s0 + steps - 1);
-    }
-  }
+  // the cached tokens' partial states: the lower half takes the anchor's part, the upper the residual's
   pdl_wait();
   __syncthreads();
   const int c_lo = range_s[0], c_hi = range_s[1];
   const int unit = bh * a.nqb + r0 / NB, qo = r0 % NB;
   const float* part = a.partials + (size_t)unit * a.pstride;
-  // common reference
-  float mine[kMergeQ];
+  float ref[kMergeQ];      // common reference
 #pragma unroll
-  for (int i = 0; i < kMergeQ; ++i) mine[i] = m[i];
+  for (int i = 0; i < kMergeQ; ++i) ref[i] = m[i];
+#pragma unroll 4
   for (int c = c_lo; c <= c_hi; ++c) {
-#pragma unroll
-    for (int i = 0; i < kMergeQ; ++i) mine[i] = fmaxf(mine[i], __ldcg(part + (size_t)c * a.pstride + qo + i));
+    const float4* mp = reinterpret_cast<const float4*>(part + (size_t)c * a.pstride + qo);
+    const float4 x = __ldcg(mp), y = __ldcg(mp + 1);
+    ref[0] = fmaxf(ref[0], x.x); ref[1] = fmaxf(ref[1], x.y); ref[2] = fmaxf(ref[2], x.z); ref[3] = fmaxf(ref[3], x.w);
+    ref[4] = fmaxf(ref[4], y.x); ref[5] = fmaxf(ref[5], y.y); ref[6] = fmaxf(ref[6], y.z); ref[7] = fmaxf(ref[7], y.w);
   }
-  float orr[kMergeQ];
+  float oc[kMergeQ];       // this thread's plane of the cached tokens
 #pragma unroll
   for (int i = 0; i < kMergeQ; ++i) {
-    if (mine[i] == -INFINITY) mine[i] = 0.f;
-    const float f = exp2f(m[i] - mine[i]);
+    if (ref[i] == -INFINITY) ref[i] = 0.f;
+    const float f = exp2f(m[i] - ref[i]);
     l[i] *= f;
     o[i] *= f;
-    orr[i] = 0.f;
+    oc[i] = 0.f;
   }
+  const bool mine = ch < D && (NRES || !half);
+#pragma unroll 2
   for (int c = c_lo; c <= c_hi; ++c) {
     const float* p = part + (size_t)c * a.pstride;
-    float f[kMergeQ];
+    const float4 m0 = __ldcg(reinterpret_cast<const float4*>(p + qo)), m1 = __ldcg(reinterpret_cast<const float4*>(p + qo) + 1);
+    const float4 l0 = __ldcg(reinterpret_cast<const float4*>(p + NB + qo)),
+                 l1 = __ldcg(reinterpret_cast<const float4*>(p + NB + qo) + 1);
+    float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
+    if (mine) {
+      const float4* xp = reinterpret_cast<const float4*>(p + 2 * NB) + (size_t)(half * (NB / 4) + qo / 4) * D + ch;
+      x0 = __ldcg(xp);
+      x1 = __ldcg(xp + D);
+    }
+    const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+    const float ll[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
+    const float xx[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
     for (int i = 0; i < kMergeQ; ++i) {
-      f[i] = exp2f(__ldcg(p + qo + i) - mine[i]);
-      l[i] = fmaf(f[i], __ldcg(p + NB + qo + i), l[i]);
-      f[i] *= NRES ? 128.f : 32768.f;   // the operands' power of two
-    }
-    if (tid < D) {
-#pragma unroll
-      for (int i4 = 0; i4 < kMergeQ / 4; ++i4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + 2 * NB) + (size_t)(qo / 4 + i4) * D + tid);
-        o[4 * i4] = fmaf(f[4 * i4], x.x, o[4 * i4]);
-        o[4 * i4 + 1] = fmaf(f[4 * i4 + 1], x.y, o[4 * i4 + 1]);
-        o[4 * i4 + 2] = fmaf(f[4 * i4 + 2], x.z, o[4 * i4 + 2]);
-        o[4 * i4 + 3] = fmaf(f[4 * i4 + 3], x.w, o[4 * i4 + 3]);
-        if (NRES) {
-          const float4 y =
-              __ldcg(reinterpret_cast<const float4*>(p + 2 * NB) + (size_t)(NB / 4 + qo / 4 + i4) * D + tid);
-          orr[4 * i4] = fmaf(256.f * f[4 * i4], y.x, orr[4 * i4]);
-          orr[4 * i4 + 1] = fmaf(256.f * f[4 * i4 + 1], y.y, orr[4 * i4 + 1]);
-          orr[4 * i4 + 2] = fmaf(256.f * f[4 * i4 + 2], y.z, orr[4 * i4 + 2]);
-          orr[4 * i4 + 3] = fmaf(256.f * f[4 * i4 + 3], y.w, orr[4 * i4 + 3]);
-        }
-      }
+      const float f = exp2f(mm[i] - ref[i]);
+      l[i] = fmaf(f, ll[i], l[i]);
+      oc[i] = fmaf(f, xx[i], oc[i]);
     }
   }
-  if (NRES && c_hi >= c_lo) {   // R^T: thread = output channel
+  // the operands' powers of two: V's anchor under a coefficient 2^-7, else 2^-15
+  const float up = NRES && !half ? 128.f : 32768.f;
+#pragma unroll
+  for (int i = 0; i < kMergeQ; ++i) oc[i] *= up;
+  if (!half) {
+#pragma unroll
+    for (int i = 0; i < kMergeQ; ++i) o[i] += oc[i];
+  }
+  if (NRES && c_hi >= c_lo) {   // R^T: a thread sums half of the channels for one output channel
     if ((a.g.mode & RQ_MODE_HADAMARD) != 0) {
-      hadamard128<kMergeQ>(orr, tid, &q_s[0][0]);
+      if (half) {
 #pragma unroll
-      for (int i = 0; i < kMergeQ; ++i) o[i] += orr[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < kMergeQ; ++i) p_s[tid][i] = orr[i];
+        for (int i = 0; i < kMergeQ; ++i) p_s[ch][i] = oc[i];
+      }
       __syncthreads();
-      if (tid < D) {
-#pragma unroll 8
-        for (int k = 0; k < D; ++k) {
-          const float r = __ldg(a.R + (size_t)k * D + tid);
+      float t[kMergeQ];
+#pragma unroll
+      for (int i = 0; i < kMergeQ; ++i) t[i] = half ? 0.f : p_s[ch][i];
+      __syncthreads();
+      hadamard128<kMergeQ>(t, tid, &q_s[0][0]);   // threads >= 128 only take part in its barriers
+      if (!half) {
+#pragma unroll
+        for (int i = 0; i < kMergeQ; ++i) o[i] += t[i];
+      }
+    } else {
+      if (half) {
+#pragma unroll
+        for (int i = 0; i < kMergeQ; ++i) p_s[ch][i] = oc[i];
+      }
+      __syncthreads();
+      if (ch < D) {
+#pragma unroll 16
+        for (int k = half * (D / 2); k < (half + 1) * (D / 2); ++k) {
+          const float r = __ldg(a.R + (size_t)k * D + ch);
           const float4 x = *reinterpret_cast<const float4*>(p_s[k]), y = *reinterpret_cast<const float4*>(p_s[k] + 4);
           o[0] = fmaf(r, x.x, o[0]); o[1] = fmaf(r, x.y, o[1]); o[2] = fmaf(r, x.z, o[2]); o[3] = fmaf(r, x.w, o[3]);
           o[4] = fmaf(r, y.x, o[4]); o[5] = fmaf(r, y.y, o[5]); o[6] = fmaf(r, y.z, o[6]); o[7] = fmaf(r, y.w, o[7]);
@@ -1328,12 +1384,18 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(TreeArgs a, int ctas) {
       }
     }
   }
-  if (tid < D) {
-    __nv_bfloat16* op = a.out + ((size_t)bh * a.M + r0) * D + tid;
+  __syncthreads();
+  if (half) {
+#pragma unroll
+    for (int i = 0; i < kMergeQ; ++i) h_s[ch][i] = o[i];
+  }
+  __syncthreads();
+  if (!half && ch < D) {
+    __nv_bfloat16* op = a.out + ((size_t)bh * a.M + r0) * D + ch;
 #pragma unroll
     for (int i = 0; i < kMergeQ; ++i)
-      if (i < nq && (r0 + i) % a.T < cnt)
-        op[(size_t)i * D] = __float2bfloat16_rn(l[i] != 0.f ? o[i] / l[i] : 0.f);   // no key seen: zero; NaN stays
+      if (i < nq && (r0 + i) % a.T < cnt)   // no key seen: zero; NaN stays
+        op[(size_t)i * D] = __float2bfloat16_rn(l[i] != 0.f ? (o[i] + h_s[ch][i]) / l[i] : 0.f);
   }
 }
 
@@ -1351,7 +1413,7 @@ cudaError_t launch_tree_t(const TreeArgs& args, int num_sms, cudaStream_t stream
   e = launch_dependent(kern, dim3(num_sms), dim3(kTreeThreads), (size_t)C::SMEM, stream, a);
   if (e != cudaSuccess) return e;
   return launch_dependent(tree_merge_kernel<D, NRES, NB>, dim3(a.batch * a.g.H * ((a.M + kMergeQ - 1) / kMergeQ)),
-                          dim3(128), 0, stream, a, num_sms);
+                          dim3(kMergeThreads), 0, stream, a, num_sms);
 }
 
 template <int D, int GS, int NRES>
