@@ -4,9 +4,9 @@
 //   (a', b') = m (a cos - b sin, b cos + a sin);
 // the inverse call negates the angle, which is the transposed map and so the
 // gradient.  The fraction of a turn of position p is p * F mod 1 with F = f / 2 pi
-// as a 64-bit binary fraction: one wrapping integer product, exact for every
-// int32 position up to the rounding of F (2^-65 of a turn a position, 2^-34 at
-// the farthest).  sin and cos are then taken of a reduced float32 argument.
+// as a 64-bit binary fraction: one wrapping integer product, exact but for the
+// rounding of F, taken in float64 (2^-55 of a turn a position, 2^-24 at the farthest).
+// sin and cos are then taken of a reduced float32 argument.
 //
 // Memory-bound: every element is read and written once.
 #include <cmath>
@@ -45,12 +45,142 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __
 template <> __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ float from_f(float v) { return v; }
 
-// magnitude * (cos, sin) of pair i at position p
+// magnitude * (cos, sin) of pair i at position p.  The fraction of a turn is split in
+// integers into the nearest quarter and a rest of at most an eighth, |y| <= pi / 4 in radians,
+// where the Taylor series to y^9 and y^10 are off by less than 2^-29 (of sin y / y) and 2^-32.
 __device__ __forceinline__ float2 turn_of(const RopeArgs& a, int i, int p) {
-  const long long frac = (long long)((unsigned long long)(long long)p * a.turn[i]);   // mod one turn
-  float s, c;
-  sincospif((float)(int)(frac >> 32) * 0x1p-31f, &s, &c);   // top 32 bits: half turns / 2^31
-  return make_float2(c * a.mag, s * a.mag);
+  const unsigned long long frac = (unsigned long long)(long long)p * a.turn[i];   // mod one turn
+  const unsigned q = (unsigned)((frac + (1ull << 61)) >> 62);
+  const int rest = (int)((long long)(frac - ((unsigned long long)q << 62)) >> 32);   // 2^-32 turns
+  const float y = (float)rest * 1.46291807926715968e-9f;                             // 2 pi / 2^32
+  const float z = y * y;
+  const float s = y * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), 1.f);
+  const float c =
+      fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  const float cc = q & 1 ? -s : c, ss = q & 1 ? c : s;   // a quarter turn: (cos, sin) -> (-sin, cos)
+  const float sign = q & 2 ? -a.mag : a.mag;
+  return make_float2(cc * sign, ss * sign);
+}
+__device__ __forceinline__ int position(const RopeArgs& a, int64_t token, int b, int t) {
+  return (int)((unsigned)(a.start ? a.start[b] : 0) + (unsigned)(a.offsets ? a.offsets[token] : t));
+}
+
+// 16 bytes as V floats and back
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+  static constexpr int V = 4;
+  static __device__ __forceinline__ void load(const uint4& u, float* f) {
+    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 store(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+template <> struct Vec<__nv_bfloat16> {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ void load(const uint4& u, float* f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 store(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <> struct Vec<__half> {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ void load(const uint4& u, float* f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = x.x;
+      f[2 * i + 1] = x.y;
+    }
+  }
+  static __device__ __forceinline__ uint4 store(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// The vector path: everything on 16-byte boundaries.  A thread takes V pairs of one token --
+// two 16-byte pieces, c and c + r / 2 (halves) or neighbours (interleaved) -- and walks along
+// heads with the same sines and cosines, kHeads of them in flight at a time; further threads of
+// the token copy the channels that do not turn.
+constexpr int kHeads = 4;
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kThreads) rope_vec_kernel(RopeArgs a) {
+  constexpr int V = Vec<T>::V;
+  const int turns = a.r / (2 * V), work = turns + (a.d - a.r) / V;    // threads a token
+  const unsigned idx = blockIdx.x * (unsigned)kThreads + threadIdx.x;
+  const unsigned token = idx / (unsigned)work;
+  if (token >= (unsigned)a.batch * (unsigned)a.n) return;
+  const int u = (int)(idx % (unsigned)work), b = (int)(token / (unsigned)a.n), t = (int)(token % (unsigned)a.n);
+  const int heads = a.x[0].heads + a.x[1].heads;
+  const bool turn = u < turns;
+  const int c0 = turn ? (INTER ? 2 * V * u : V * u) : a.r + V * (u - turns), step = INTER ? V : a.r / 2;
+  float cs[V], sn[V];
+  if (turn) {
+    const int pos = position(a, token, b, t);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float2 x = turn_of(a, V * u + i, pos);
+      cs[i] = x.x;
+      sn[i] = x.y;
+    }
+  }
+  const T *in0 = static_cast<const T*>(a.x[0].in) + b * a.x[0].in_row + t * a.x[0].in_token + c0,
+          *in1 = static_cast<const T*>(a.x[1].in) + b * a.x[1].in_row + t * a.x[1].in_token + c0;
+  T *out0 = static_cast<T*>(a.x[0].out) + b * a.x[0].out_row + t * a.x[0].out_token + c0,
+    *out1 = static_cast<T*>(a.x[1].out) + b * a.x[1].out_row + t * a.x[1].out_token + c0;
+  const int per = (heads + gridDim.y - 1) / gridDim.y, h0 = blockIdx.y * per, h1 = min(heads, h0 + per);
+  for (int h = h0; h < h1; h += kHeads) {
+    uint4 lo[kHeads], hi[kHeads];
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      if (h + k >= h1) break;
+      const int hh = h + k - a.x[0].heads;
+      const T* p = hh < 0 ? in0 + (h + k) * a.x[0].in_head : in1 + hh * a.x[1].in_head;
+      lo[k] = *reinterpret_cast<const uint4*>(p);
+      if (turn) hi[k] = *reinterpret_cast<const uint4*>(p + step);
+    }
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      if (h + k >= h1) break;
+      const int hh = h + k - a.x[0].heads;
+      T* p = hh < 0 ? out0 + (h + k) * a.x[0].out_head : out1 + hh * a.x[1].out_head;
+      if (turn) {
+        float x[2 * V], y[2 * V];
+        Vec<T>::load(lo[k], x);
+        Vec<T>::load(hi[k], x + V);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = INTER ? 2 * i : i, f = INTER ? 2 * i + 1 : i + V;
+          y[e] = x[e] * cs[i] - x[f] * sn[i];
+          y[f] = x[f] * cs[i] + x[e] * sn[i];
+        }
+        *reinterpret_cast<uint4*>(p) = Vec<T>::store(y);
+        *reinterpret_cast<uint4*>(p + step) = Vec<T>::store(y + V);
+      } else {
+        *reinterpret_cast<uint4*>(p) = lo[k];
+      }
+    }
+  }
 }
 
 // One thread per (token, pair or copied channel), looping over its heads.
@@ -65,8 +195,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
   float2 cs = make_float2(1.f, 0.f);
   int c0, c1 = -1;
   if (u < half) {
-    const int pos = (int)((unsigned)(a.start ? a.start[b] : 0) + (unsigned)(a.offsets ? a.offsets[token] : t));
-    cs = turn_of(a, u, pos);
+    cs = turn_of(a, u, position(a, token, b, t));
     c0 = a.inter ? 2 * u : u;
     c1 = a.inter ? 2 * u + 1 : u + half;
   } else {
@@ -87,12 +216,42 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
   }
 }
 
+// Whether every vector of 16 bytes that the vector path touches starts on a 16-byte boundary.
 template <typename T>
-cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
+bool vectors_fit(const RopeArgs& a) {
+  constexpr int V = Vec<T>::V;
+  if (a.d % V || a.r % (2 * V)) return false;
+  for (const RopeTensor& x : a.x) {
+    if (!x.heads) continue;
+    if (reinterpret_cast<uintptr_t>(x.in) % 16 || reinterpret_cast<uintptr_t>(x.out) % 16) return false;
+    for (int64_t s : {x.in_row, x.in_head, x.in_token, x.out_row, x.out_head, x.out_token})
+      if (s % V) return false;
+  }
+  return true;
+}
+
+template <typename T>
+cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
+  const int heads = a.x[0].heads + a.x[1].heads;
+  if (vectors_fit<T>(a)) {
+    constexpr int V = Vec<T>::V;
+    const int64_t threads = (int64_t)a.batch * a.n * (a.r / (2 * V) + (a.d - a.r) / V);
+    if (threads <= 0x7fffff00) {   // 32-bit thread numbers
+      const int blocks = (int)((threads + kThreads - 1) / kThreads);
+      // heads split over gridDim.y only as far as the tokens alone do not fill the GPU (a split
+      // repeats the sines): some 8 blocks an SM
+      int split = num_sms * 8 / blocks;
+      split = split < 1 ? 1 : (split > heads ? heads : split);
+      if (a.inter)
+        rope_vec_kernel<T, true><<<dim3(blocks, split), kThreads, 0, stream>>>(a);
+      else
+        rope_vec_kernel<T, false><<<dim3(blocks, split), kThreads, 0, stream>>>(a);
+      return cudaGetLastError();
+    }
+  }
   const int64_t work = (int64_t)a.batch * a.n * (a.r / 2 + a.d - a.r);
   const int64_t blocks = (work + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorNotSupported;
-  const int heads = a.x[0].heads + a.x[1].heads;
   rope_kernel<T><<<dim3((unsigned)blocks, heads < 8 ? heads : 8), kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
@@ -165,7 +324,12 @@ extern "C" rq_status rq_rope(const rq_rope_config* cfg, int32_t dtype, int32_t b
   a.inter = cfg->interleaved != 0;
   a.mag = cfg->magnitude == 0.0 ? 1.f : (float)cfg->magnitude;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == RQ_BF16 ? launch_rope<__nv_bfloat16>(a, st)
-                                         : (dtype == RQ_F16 ? launch_rope<__half>(a, st) : launch_rope<float>(a, st));
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return RQ_ERR_CUDA;
+  const cudaError_t e = dtype == RQ_BF16  ? launch_rope<__nv_bfloat16>(a, sms, st)
+                        : dtype == RQ_F16 ? launch_rope<__half>(a, sms, st)
+                                          : launch_rope<float>(a, sms, st);
   return e == cudaSuccess ? RQ_OK : (e == cudaErrorNotSupported ? RQ_ERR_UNSUPPORTED : RQ_ERR_CUDA);
 }

@@ -67,7 +67,6 @@ constexpr int kTreeStep = 128;               // tokens per step: two layout tile
 constexpr int kTreeThreads = 20 * 32;
 constexpr int kTreeRows = RQ_MAX_DECODE_BATCH;
 constexpr int kMergeQ = 8;                   // queries per merge CTA
-constexpr int kPrepQ = 8;                    // queries per prep CTA
 constexpr float kHead = 6.f;                 // a row maximum's weight is 2^kHead
 constexpr float kTop = 14.f;                 // largest log2 weight before the reference moves
 
@@ -353,106 +352,127 @@ struct TreeCfg {
 };
 
 // ---- query prep --------------------------------------------------------------------
-// One CTA per kPrepQ queries of a unit: x and R x as f16 times a power of two of the
-// query's own (its largest component to 2^10 .. 2^11: R keeps norms, so both stay below
-// 2^15), in the layout of the B operand.
+// One CTA per unit: x and R x as f16 times a power of two of the query's own (its largest
+// component to 2^10 .. 2^11: R keeps norms, so both stay below 2^15), in the layout of the B
+// operand.  x is BF16 and so exact; R x is a product on the 16-bit tensor cores with R as two
+// BF16 pieces (16 bits, against the 11 of its result), summed in float32: 8 warps with 16 rows
+// of R each in registers, one pass over the queries.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// two floats as BF16 pairs: the rounded values and the rounded remainders
+__device__ __forceinline__ void bf16_pieces(float2 x, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+  const float2 f = __bfloat1622float2(h);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(x.x - f.x, x.y - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
 template <int D, int NRES, int NB>
 __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
-  constexpr int RPW = D / 8;
   constexpr int PL = 1 + NRES;
   constexpr int IMG = PL * (D / 16) * NB * 32;
-  __shared__ __align__(16) float q_s[kPrepQ][128];
-  __shared__ float r_s[kPrepQ][128];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int unit = blockIdx.x / (NB / kPrepQ), q0 = blockIdx.x % (NB / kPrepQ) * kPrepQ;
-  const int qb = unit % a.nqb, bh = unit / a.nqb, b = bh / a.g.H;
+  constexpr int PITCH = D + 8;             // BF16 elements: rows 4 banks apart
+  constexpr int RPITCH = D + 4;
+  __shared__ __align__(16) __nv_bfloat16 q_s[NB][PITCH];
+  __shared__ __align__(16) float r_s[NRES ? NB : 1][RPITCH];
+  __shared__ float up_s[NB];               // the query's power of two
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  const int unit = blockIdx.x, qb = unit % a.nqb, bh = unit / a.nqb, b = bh / a.g.H;
   const bool hadamard = (a.g.mode & RQ_MODE_HADAMARD) != 0;
-  float4 rv[NRES ? RPW : 1];
-  if (NRES && !hadamard) {   // R does not change while the cache is used: before the wait
+  uint32_t hi[NRES ? D / 16 : 1][4], lo[NRES ? D / 16 : 1][4];
+  if (NRES && !hadamard && warp < D / 16) {   // R does not change while the cache is used: before the wait
+    const float* rp = a.R + (size_t)(16 * warp + g) * D + 2 * t4;
 #pragma unroll
-    for (int v = 0; v < RPW; ++v)
-      rv[v] = lane < D / 4 ? __ldg(reinterpret_cast<const float4*>(a.R + (size_t)(warp + 8 * v) * D) + lane)
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)   // rows g, g + 8; columns 2 t4, 2 t4 + 8
+        bf16_pieces(__ldg(reinterpret_cast<const float2*>(rp + (i & 1) * 8 * D + 16 * k + (i >> 1) * 8)), hi[k][i], lo[k][i]);
   }
   pdl_wait();
   pdl_launch_dependents();   // what ran before the call is complete: the next kernel may read the cache
   const int cnt = a.counts ? clamp_len(a.counts[b], a.T) : a.T;
   const __nv_bfloat16* qu = a.q + ((size_t)bh * a.M + (size_t)qb * NB) * D;
   const int rows = min(NB, a.M - qb * NB);
-  {   // one warp per query; a query that is not finite keeps the scale 1 and stays so
-    const int r = q0 + warp;
+  // one warp per query: its values (zeros for a node not in use), its power of two; a query that
+  // is not finite keeps the scale 1 and stays so
+#pragma unroll 4
+  for (int r = warp; r < NB; r += 8) {
     const bool on = r < rows && (qb * NB + r) % a.T < cnt;
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (on && lane < D / 4) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(qu + (size_t)r * D) + lane);
-      x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-      x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-    }
-    float big = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    uint2 v = make_uint2(0u, 0u);
+    if (on && lane < D / 4) v = __ldg(reinterpret_cast<const uint2*>(qu + (size_t)r * D) + lane);
+    if (lane < D / 4) *reinterpret_cast<uint2*>(&q_s[r][4 * lane]) = v;
+    // magnitudes of BF16 numbers compare as integers
+    uint32_t big = max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu));
+    big = __reduce_max_sync(0xffffffffu, big);
     int e = 11;
-    if (big > 0.f && isfinite(big)) frexpf(big, &e);   // big = f 2^e, f in [0.5, 1)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane < D / 4) q_s[warp][4 * lane + i] = ldexpf(x[i], 11 - e);
-    if (lane == 0) a.q_scale[(size_t)unit * NB + r] = ldexpf(a.qscale, e - 11 + kScaleK);
+    if (big > 0 && big < 0x7F80u) frexpf(__uint_as_float(big << 16), &e);   // f 2^e, f in [0.5, 1)
+    e = max(e, -115);                                                       // 2^(11 - e) stays finite
+    if (lane == 0) {
+      up_s[r] = ldexpf(1.f, 11 - e);
+      a.q_scale[(size_t)unit * NB + r] = ldexpf(a.qscale, e - 11 + kScaleK);
+    }
   }
   __syncthreads();
   if (NRES && hadamard) {
     // one warp per query: lane holds channels lane, lane + 32, ...; stages h = 1 .. 64
-    float v[4];
+    for (int r = warp; r < NB; r += 8) {
+      float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = q_s[warp][(lane + 32 * i) % D];
+      for (int i = 0; i < 4; ++i) v[i] = __bfloat162float(q_s[r][(lane + 32 * i) % D]);
 #pragma unroll
-    for (int h = 1; h < 32; h <<= 1)
+      for (int h = 1; h < 32; h <<= 1)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = __shfl_xor_sync(0xffffffffu, v[i], h);
-        v[i] = (lane & h) ? p - v[i] : v[i] + p;
+        for (int i = 0; i < 4; ++i) {
+          const float p = __shfl_xor_sync(0xffffffffu, v[i], h);
+          v[i] = (lane & h) ? p - v[i] : v[i] + p;
+        }
+      const float s0 = v[0] + v[1], s1 = v[0] - v[1], s2 = v[2] + v[3], s3 = v[2] - v[3];
+      if (D == 128) {
+        r_s[r][lane] = (s0 + s2) * kInvSqrt128;
+        r_s[r][lane + 32] = (s1 + s3) * kInvSqrt128;
+        r_s[r][(lane + 64) % D] = (s0 - s2) * kInvSqrt128;
+        r_s[r][(lane + 96) % D] = (s1 - s3) * kInvSqrt128;
       }
-    const float s0 = v[0] + v[1], s1 = v[0] - v[1], s2 = v[2] + v[3], s3 = v[2] - v[3];
-    if (D == 128) {
-      r_s[warp][lane] = (s0 + s2) * kInvSqrt128;
-      r_s[warp][lane + 32] = (s1 + s3) * kInvSqrt128;
-      r_s[warp][lane + 64] = (s0 - s2) * kInvSqrt128;
-      r_s[warp][lane + 96] = (s1 - s3) * kInvSqrt128;
     }
     __syncthreads();
   } else if (NRES) {
-    // (R x)[row]: lane partials of the warp's rows, then a reduce-scatter over the lanes
-    for (int qi = 0; qi < kPrepQ; ++qi) {
-      const float4 x = lane < D / 4 ? reinterpret_cast<const float4*>(q_s[qi])[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-      float pv[16];
+    if (warp < D / 16) {
+#pragma unroll 2
+      for (int n = 0; n < NB; n += 8) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int v = 0; v < 16; ++v)
-        pv[v] = v < RPW ? fmaf(rv[v].x, x.x, fmaf(rv[v].y, x.y, fmaf(rv[v].z, x.z, rv[v].w * x.w))) : 0.f;
-#pragma unroll
-      for (int o = 16, n = 8; n >= 1; o >>= 1, n >>= 1) {
-        const bool up = (lane & o) != 0;
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-          const float send = up ? pv[i] : pv[i + n], keep = up ? pv[i + n] : pv[i];
-          pv[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t* bp = reinterpret_cast<const uint32_t*>(&q_s[n + g][16 * k + 2 * t4]);
+          const uint32_t b0 = bp[0], b1 = bp[4];
+          mma_bf16(d, hi[k], b0, b1);
+          mma_bf16(d, lo[k], b0, b1);
         }
+        const int c = 16 * warp + g, q = n + 2 * t4;
+        r_s[q][c] = d[0];
+        r_s[q + 1][c] = d[1];
+        r_s[q][c + 8] = d[2];
+        r_s[q + 1][c + 8] = d[3];
       }
-      pv[0] += __shfl_xor_sync(0xffffffffu, pv[0], 1);
-      const int row = warp + 8 * (lane >> 1);
-      if ((lane & 1) == 0 && row < D) r_s[qi][row] = pv[0];
     }
     __syncthreads();
   }
-  // the operand: 8 channels (16 bytes) a thread, rows of 64 channels, swizzled
+  // the operand: 8 channels (16 bytes) a thread, 16 to a block of 32 bytes a query, swizzled
   uint8_t* img = a.packs + (size_t)unit * IMG;
-  for (int i = tid; i < PL * kPrepQ * (D / 8); i += 256) {
-    const int c = i % (D / 8), qi = i / (D / 8) % kPrepQ, pl = i / (D / 8 * kPrepQ);
-    const float* x = pl ? r_s[qi] : q_s[qi];
+  for (int i = tid; i < PL * NB * (D / 8); i += 256) {
+    const int c = i % (D / 8), r = i / (D / 8) % NB, pl = i / (D / 8 * NB);
+    const float up = up_s[r];
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int lo = k_channel<D>(4 * c + j, pl != 0);
-      w[j] = f16x2(x[lo], x[lo + (pl ? 8 : 4)]);
+      const int ch = k_channel<D>(4 * c + j, pl != 0);
+      const float x0 = pl ? r_s[NRES ? r : 0][ch] : __bfloat162float(q_s[r][ch]);
+      const float x1 = pl ? r_s[NRES ? r : 0][ch + 8] : __bfloat162float(q_s[r][ch + 4]);
+      w[j] = f16x2(x0 * up, x1 * up);
     }
-    const int r = q0 + qi;
     *reinterpret_cast<uint4*>(img + ((pl * (D / 16) + (c >> 1)) * NB + r) * 32 + (((c & 1) ^ ((r >> 2) & 1)) << 4)) =
         make_uint4(w[0], w[1], w[2], w[3]);
   }
@@ -1408,7 +1428,7 @@ cudaError_t launch_tree_t(const TreeArgs& args, int num_sms, cudaStream_t stream
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const int units = a.batch * a.g.H * a.nqb;
-  e = launch_dependent(tree_prep_kernel<D, NRES, NB>, dim3(units * (NB / kPrepQ)), dim3(256), 0, stream, a);
+  e = launch_dependent(tree_prep_kernel<D, NRES, NB>, dim3(units), dim3(256), 0, stream, a);
   if (e != cudaSuccess) return e;
   e = launch_dependent(kern, dim3(num_sms), dim3(kTreeThreads), (size_t)C::SMEM, stream, a);
   if (e != cudaSuccess) return e;

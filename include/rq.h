@@ -363,7 +363,8 @@ size_t rq_tree_workspace_bytes(const rq_config* cfg, int32_t batch, int32_t n_no
  * A K or V that a node's mask hides does not enter that node's result, not even
  * when it is infinite or NaN.  q is scaled per node by a power of two and kept
  * in 16-bit floating point (11 significant bits), as are the rebuilt K/V and the
- * softmax weights; scores, softmax sums and accumulators are float32.
+ * softmax weights (rebuilt K/V up to 65504); scores, softmax sums and
+ * accumulators are float32.
  * With T = 1 and a mask that names the token itself this is
  * rq_decode_attention with a BF16 result.
  * Chained caches (RQ_MODE_CHAINED) are read as rq_decode_attention reads them.
@@ -494,8 +495,8 @@ typedef struct rq_rope_tensor {
  * are start[b] + offsets[b][t], offsets NULL: start[b] + t, so with start =
  * seq_lens a prompt, a decoded token (n = 1) or the nodes of a drafted tree
  * (offsets = their depths) sit where they belong.  Angles are taken modulo a
- * turn in 64-bit fixed point: exact for every int32 position.  Arithmetic is
- * float32, rounded once to the tensors' type.
+ * turn in 64-bit fixed point (off by 2^-55 of a turn a position, 2^-24 at the
+ * farthest).  Arithmetic is float32, rounded once to the tensors' type.
  *   dtype    rq_dtype of every tensor
  *   q, k     host; k (or q) may be NULL
  *   start    device int32 [batch], or NULL: zeros
