@@ -14,9 +14,9 @@
 //   values  O^T [channels x NB] += V'^T P^T     (anchor and residual part apart)
 // K' and V'^T are dequantized into registers and stored to tensor memory as the A operand
 // (f16, one token or channel per lane): dequantized data never touches shared memory.
-// Roles (20 warps, in groups of four, one per 32 lanes): K, softmax, V of the anchor, V of the
-// residual (anchor loop: the other half of the anchor's), and a group with the copy warp and
-// one warp for each kind of product.
+// Roles (24 warps, in groups of four, one per 32 lanes): K, softmax, two for V of the anchor, V of
+// the residual (idle in the anchor loop), and a group with the copy warp and one warp for each
+// kind of product.
 //
 // Dequantization: an f16 whose bits are an integer n < 1024 has the value n 2^-24, so masking a
 // code word leaves codes times 2^(p - 24), p the field's first bit; one fused multiply-add with
@@ -64,9 +64,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTreeStep = 128;               // tokens per step: two layout tiles
-constexpr int kTreeThreads = 20 * 32;
+constexpr int kTreeThreads = 24 * 32;
 constexpr int kTreeRows = RQ_MAX_DECODE_BATCH;
-constexpr int kMergeQ = 8;                   // queries per merge CTA
 constexpr float kHead = 6.f;                 // a row maximum's weight is 2^kHead
 constexpr float kTop = 14.f;                 // largest log2 weight before the reference moves
 
@@ -342,11 +341,11 @@ struct TreeCfg {
   static constexpr int SCOLS = 2 * NB;                     // Sa, Sr
   static_assert(S0 + SCOLS <= 512, "tensor memory");
   static_assert(SMEM <= 227 * 1024 - 5120, "shared memory");
-  // registers a thread: 96 at launch (5 groups: 480), then softmax, the three dequantizers, copies
+  // registers a thread: 80 at launch (6 groups: 480), then softmax, the four dequantizers, copies
   static constexpr int REGS = NB == 64 ? 176 : 136;
-  static constexpr int REGD = NB == 64 ? 80 : 96;
-  static constexpr int REGP = 56;
-  static_assert(REGS + 3 * REGD + REGP <= 480, "registers");
+  static constexpr int REGD = NB == 64 ? 64 : 72;
+  static constexpr int REGP = NB == 64 ? 48 : 56;
+  static_assert(REGS + 4 * REGD + REGP <= 480, "registers");
   // floats of a partial: m[NB], l[NB], O as [plane][NB/4][D][4]
   static constexpr int PSTRIDE = 2 * NB + PL * NB * D;
 };
@@ -506,11 +505,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
 
   tree_rows(a, &rows_s);
   if (tid == 32) {
-    for (int i = 0; i < ST; ++i) { mbar_init(&full_bar[i], 1); mbar_init(&empty_bar[i], NRES ? 16 : 12); }
+    for (int i = 0; i < ST; ++i) { mbar_init(&full_bar[i], 1); mbar_init(&empty_bar[i], NRES ? 20 : 12); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull_bar[i], 1); mbar_init(&qempty_bar[i], 1);
       mbar_init(&kfull_bar[i], 4); mbar_init(&kempty_bar[i], 1);
-      mbar_init(&vfull_bar[i], NRES ? 4 : 8); mbar_init(&vempty_bar[i], 1);
+      mbar_init(&vfull_bar[i], i ? 4 : 8); mbar_init(&vempty_bar[i], 1);
     }
     mbar_init(&sfull_bar, 1); mbar_init(&sempty_bar, 4);
     mbar_init(&pfull_bar, 4); mbar_init(&pempty_bar, 1);
@@ -526,7 +525,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     pdl_wait();
     return;
   }
-  if (warp == 17) {
+  if (warp == 21) {
     tc_alloc(&tmem_s, 512);
     tc_relinquish();
     tc_before();
@@ -555,7 +554,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
   auto v_role = [&](auto plane, int part) {
     constexpr int pl = decltype(plane)::value;
     const int w4 = warp & 3, lt = tid & 127;
-    auto v_sync = [&]() { if (NRES) wg_sync(2 + pl); else wg_sync2(2); };   // the groups that share constants
+    auto v_sync = [&]() { if (pl) wg_sync(3); else wg_sync2(2); };   // the groups that share constants
     const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
     const int col = v_slot(lt) >> 1, hf = v_slot(lt) & 1;   // the token's place among the constants
     const int t4 = lane & 3;                                // the lane's 32 tokens: 32 t4 ..
@@ -596,7 +595,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + (pl ? C::R_CODES : C::A_CODES)) + tok * NG;
 #pragma unroll
         for (int gi = 0; gi < NG; ++gi) {
-          if (!NRES && (gi & 1) != part) continue;
+          if (pl == 0 && (gi & 1) != part) continue;
           __half2 so = __hmul2(e4m3_pair(on ? meta[gi] : (uint16_t)0), to_k);
           if (pl) so = __hmul2(so, field);
           else if (NRES) so = __hmul2(__hmul2(so, f1), f2);
@@ -626,7 +625,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
               if (NRES && pl == 0) mq[j] = cm[16 * c + 4 * j];
             }
 #pragma unroll 1
-            for (int hh = NRES ? 0 : part; hh < (NRES ? 2 : part + 1); ++hh) {
+            for (int hh = pl ? 0 : part; hh < (pl ? 2 : part + 1); ++hh) {
               if (GS == 16) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) kq[j] = tb[hh * 32 + 16 * c + 4 * j];
@@ -675,9 +674,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     }
   };
 
-  if (warp >= 16) {
+  if (warp >= 20) {
     reg_dec<C::REGP>();
-  if (warp == 16) {
+  if (warp == 20) {
     // ================= copies =================
     if (lane == 0) {
       const uint64_t pol = l2_evict_first_policy();
@@ -747,7 +746,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       }
     }
     __syncwarp();
-  } else if (warp == 17) {
+  } else if (warp == 21) {
     // ================= products: scores =================
     const uint32_t q_lo = desc_lo(smem_u32(q_img));
     int seg = -1;
@@ -782,7 +781,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     if (elect_one()) tc_commit(&drain_bar[0]);
     wait(&drain_bar[0], 0);
     __syncwarp();
-  } else if (warp == 18) {
+  } else if (warp == 22) {
     // ================= products: values =================
     const uint32_t p_lo = desc_lo(smem_u32(p_buf));
 #pragma unroll 1
@@ -1021,7 +1020,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       }
     }
   } else {
-    if (C::REGD < 96) reg_dec<C::REGD>();
+    reg_dec<C::REGD>();
     if (warp < 4) {
     // ================= K: rows of tokens =================
     const int tau = warp >> 1;                              // the warp's tile of the step
@@ -1143,62 +1142,91 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       if (lane == 0) mbar_arrive(&empty_bar[st]);
       if (++st == ST) { st = 0; par ^= 1; }
     }
-    } else if (warp < 12) {
-      v_role(std::integral_constant<int, 0>{}, 0);
-    } else {
-      v_role(std::integral_constant<int, NRES>{}, 1);
+    } else if (warp < 16) {
+      v_role(std::integral_constant<int, 0>{}, warp >= 12);
+    } else if (NRES) {
+      v_role(std::integral_constant<int, NRES>{}, 0);
     }
   }
   tc_before();
   __syncthreads();
-  if (warp == 17) {
+  if (warp == 21) {
     tc_after();
     tc_dealloc(tmem, 512);
   }
 }
 
 // ---- merge -------------------------------------------------------------------------
-// One CTA per kMergeQ queries of a (row, KV head).  The drafted tokens first (BF16 keys and
-// values through shared memory, float32 arithmetic; before the wait: nothing of it depends on
-// the streaming kernel), then the partial states, R^T, the quotient.  Two threads share a
-// channel (or a key): the loads of each part are all in flight at once, as the kernel is
-// nothing but a chain of latencies.
+// One CTA per MQ queries of a (row, KV head).  The drafted tokens first (before the wait:
+// nothing of it depends on the streaming kernel), then the partial states, R^T, the quotient.
+// Scores of the draft are products of BF16 numbers, exact on the 16-bit tensor cores with
+// float32 sums; its values are added in float32, as a hidden one may be infinite or NaN and must
+// not enter.  R^T is a product with both sides as two BF16 pieces (2^-16 against the result's
+// 2^-9).  The kernel is a chain of latencies: what a part needs is loaded together, ahead of it.
 constexpr int kMergeThreads = 256;
-constexpr int kDraftPitch = 272;       // bytes of a staged row: 16-byte reads of 8 rows hit 8 bank groups
+constexpr int kDraftPitch = 272;       // bytes of a staged row: rows 4 banks apart
+constexpr int kMergeChunk = 32;        // partial states whose weights are held at a time
 
-template <int D, int NRES, int NB>
+template <int D, int NRES, int NB, int MQ>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, int ctas) {
+  constexpr int NT = MQ / 8, PARTS = kMergeThreads / MQ;
   __shared__ TreeRowsShared rows_s;
   __shared__ __align__(16) uint8_t kv_s[128 * kDraftPitch];   // drafted keys, then values
-  __shared__ __align__(16) float q_s[128][kMergeQ];           // [channel][query]
-  __shared__ __align__(16) float p_s[128][kMergeQ];           // [key][query], then R^T's operand [channel][query]
-  __shared__ __align__(16) float h_s[128][kMergeQ];           // the upper half's share
-  __shared__ unsigned long long vis_s[kMergeQ][RQ_MAX_TREE_NODES / 64];
-  __shared__ float red_s[4][kMergeQ];
+  __shared__ __align__(16) __nv_bfloat16 q_s[MQ][D + 8];
+  __shared__ __align__(16) float p_s[128][MQ];                // [key][query], then R^T's operand [channel][query]
+  __shared__ __align__(16) float w_s[kMergeChunk][MQ];        // weights of partial states
+  __shared__ unsigned long long vis_s[MQ][RQ_MAX_TREE_NODES / 64];
+  __shared__ float red_s[kMergeThreads / 32][MQ], m_s[MQ], l_s[MQ], f_s[MQ];
   __shared__ int range_s[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = tid >> 7, ch = tid & 127;
-  const int per_bh = (a.M + kMergeQ - 1) / kMergeQ;
-  const int bh = blockIdx.x / per_bh, r0 = blockIdx.x % per_bh * kMergeQ, b = bh / a.g.H;
-  const int nq = min(kMergeQ, a.M - r0);
+  const int g = lane >> 2, t4 = lane & 3, my_q = tid % MQ, part = tid / MQ;
+  const int per_bh = (a.M + MQ - 1) / MQ;
+  const int bh = blockIdx.x / per_bh, r0 = blockIdx.x % per_bh * MQ, b = bh / a.g.H;
+  const int nq = min(MQ, a.M - r0);
+  const bool hadamard = (a.g.mode & RQ_MODE_HADAMARD) != 0, dense = NRES && !hadamard && warp < D / 16;
   const int cnt = a.counts ? clamp_len(a.counts[b], a.T) : a.T;
   const uint4* kp = reinterpret_cast<const uint4*>(a.k_new + (size_t)bh * a.T * D);
   const uint4* vp = reinterpret_cast<const uint4*>(a.v_new + (size_t)bh * a.T * D);
   constexpr int RC = D / 8;              // 16-byte pieces of a row
-  // keys j0 .. of the draft into shared memory
+  // rows j0 .. of the draft into shared memory
   auto stage = [&](const uint4* src, int j0) {
     const int n = min(128, cnt - j0) * RC;
 #pragma unroll 4
     for (int i = tid; i < n; i += kMergeThreads)
       *reinterpret_cast<uint4*>(kv_s + (i / RC) * kDraftPitch + (i % RC) * 16) = __ldg(src + (size_t)j0 * RC + i);
   };
-  const __nv_bfloat16* qp = a.q + ((size_t)bh * a.M + r0) * D;
+  // every query's value over all threads' (of one query: PARTS threads), in a fixed order
+  auto reduce = [&](float v, bool sum) {
 #pragma unroll
-  for (int i = tid; i < kMergeQ * D; i += kMergeThreads) {
-    const int qi = i / D, c = i % D;
-    q_s[c][qi] = qi < nq ? __bfloat162float(qp[(size_t)qi * D + c]) : 0.f;
+    for (int o = MQ; o < 32; o <<= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, v, o);
+      v = sum ? v + y : fmaxf(v, y);
+    }
+    __syncthreads();
+    if (lane < MQ) red_s[warp][lane] = v;
+    __syncthreads();
+    v = red_s[0][my_q];
+#pragma unroll
+    for (int w = 1; w < kMergeThreads / 32; ++w) v = sum ? v + red_s[w][my_q] : fmaxf(v, red_s[w][my_q]);
+    return v;
+  };
+  const uint4* qp = reinterpret_cast<const uint4*>(a.q + ((size_t)bh * a.M + r0) * D);
+  for (int i = tid; i < MQ * RC; i += kMergeThreads)
+    *reinterpret_cast<uint4*>(&q_s[i / RC][(i % RC) * 8]) = i / RC < nq ? __ldg(qp + i) : make_uint4(0u, 0u, 0u, 0u);
+  if (cnt > 0) stage(kp, 0);
+  // R^T, rows (output channels) 16 warp + g, + 8, as two pieces
+  uint32_t rhi[NRES ? D / 16 : 1][4], rlo[NRES ? D / 16 : 1][4];
+  if (dense) {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* rp = a.R + (size_t)(16 * k + 2 * t4 + (i >> 1) * 8) * D + 16 * warp + g + (i & 1) * 8;
+        bf16_pieces(make_float2(__ldg(rp), __ldg(rp + D)), rhi[k][i], rlo[k][i]);
+      }
   }
-  if (tid < kMergeQ * (RQ_MAX_TREE_NODES / 64)) {
-    const int qi = tid % kMergeQ, w = tid / kMergeQ, t = (r0 + qi) % a.T;
+  for (int i = tid; i < MQ * (RQ_MAX_TREE_NODES / 64); i += kMergeThreads) {
+    const int qi = i % MQ, w = i / MQ, t = (r0 + qi) % a.T;
     unsigned long long v = 0;
     if (qi < nq && t < cnt && w * 64 < cnt) {
       v = a.mask ? __ldg(a.mask + ((size_t)b * a.T + t) * a.words + w)
@@ -1207,7 +1235,10 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, i
     }
     vis_s[qi][w] = v;
   }
-  if (cnt > 0) stage(kp, 0);
+  if (tid < MQ) {
+    m_s[tid] = -INFINITY;
+    l_s[tid] = 0.f;
+  }
   tree_rows(a, &rows_s);
   __syncthreads();
   if (tid == 0) {   // the CTAs that hold a partial state of this unit
@@ -1223,199 +1254,198 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, i
     }
   }
 
-  // m, l: of the whole draft, in every thread; o: this thread's channel, keys of its half
-  float m[kMergeQ], l[kMergeQ], o[kMergeQ];
+  float o[MQ];            // this thread's channel: drafted values of its half of the tokens
 #pragma unroll
-  for (int i = 0; i < kMergeQ; ++i) { m[i] = -INFINITY; l[i] = 0.f; o[i] = 0.f; }
+  for (int i = 0; i < MQ; ++i) o[i] = 0.f;
 #pragma unroll 1
   for (int j0 = 0; j0 < cnt; j0 += 128) {
-    const int nk = min(128, cnt - j0), key = tid & 127;   // key: this thread's, half of its channels
+    const int nk = min(128, cnt - j0);
     if (j0) {
       __syncthreads();
       stage(kp, j0);
       __syncthreads();
     }
-    float s[kMergeQ];
+    if (16 * warp < nk) {   // scores of 16 keys a warp
+      float d[NT][4];
 #pragma unroll
-    for (int i = 0; i < kMergeQ; ++i) s[i] = 0.f;
-    if (key < nk) {
-#pragma unroll 2
-      for (int c = half * (RC / 2); c < (half + 1) * (RC / 2); ++c) {
-        const uint4 v = *reinterpret_cast<const uint4*>(kv_s + key * kDraftPitch + c * 16);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+      const uint32_t* k0 = reinterpret_cast<const uint32_t*>(kv_s + (16 * warp + g) * kDraftPitch) + t4;
+      const uint32_t* k1 = k0 + 8 * kDraftPitch / 4;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float k = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-          const float4 x = *reinterpret_cast<const float4*>(q_s[8 * c + e]),
-                       y = *reinterpret_cast<const float4*>(q_s[8 * c + e] + 4);
-          s[0] = fmaf(k, x.x, s[0]); s[1] = fmaf(k, x.y, s[1]); s[2] = fmaf(k, x.z, s[2]); s[3] = fmaf(k, x.w, s[3]);
-          s[4] = fmaf(k, y.x, s[4]); s[5] = fmaf(k, y.y, s[5]); s[6] = fmaf(k, y.z, s[6]); s[7] = fmaf(k, y.w, s[7]);
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t ak[4] = {k0[8 * k], k1[8 * k], k0[8 * k + 4], k1[8 * k + 4]};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint32_t* bp = reinterpret_cast<const uint32_t*>(&q_s[8 * n + g][16 * k + 2 * t4]);
+          mma_bf16(d[n], ak, bp[0], bp[4]);
         }
       }
-    }
-    if (half) {
 #pragma unroll
-      for (int i = 0; i < kMergeQ; ++i) h_s[key][i] = s[i];
+      for (int n = 0; n < NT; ++n) {
+        *reinterpret_cast<float2*>(&p_s[16 * warp + g][8 * n + 2 * t4]) = make_float2(d[n][0], d[n][1]);
+        *reinterpret_cast<float2*>(&p_s[16 * warp + g + 8][8 * n + 2 * t4]) = make_float2(d[n][2], d[n][3]);
+      }
     }
     __syncthreads();
     stage(vp, j0);     // the keys are used up
-    if (!half) {
-#pragma unroll
-      for (int i = 0; i < kMergeQ; ++i) {
-        const bool on = key < nk && ((vis_s[i][(j0 + key) >> 6] >> ((j0 + key) & 63)) & 1);
-        s[i] = on ? (s[i] + h_s[key][i]) * a.qscale : -INFINITY;
-        float v = s[i];
-#pragma unroll
-        for (int f = 16; f > 0; f >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, f));
-        if (lane == 0) red_s[warp][i] = v;
-      }
+    auto seen = [&](int k) { return (vis_s[my_q][(j0 + k) >> 6] >> ((j0 + k) & 63)) & 1; };
+    float mx = -INFINITY;
+    for (int k = part; k < nk; k += PARTS)
+      if (seen(k)) mx = fmaxf(mx, p_s[k][my_q] * a.qscale);
+    const float old = m_s[my_q], now = fmaxf(old, reduce(mx, false));   // its barriers: staged, m_s read
+    const float ref = now == -INFINITY ? 0.f : now;
+    float sum = 0.f;
+    for (int k = part; k < nk; k += PARTS) {
+      const float p = seen(k) ? exp2f(p_s[k][my_q] * a.qscale - ref) : 0.f;   // a NaN score stays
+      p_s[k][my_q] = p;
+      sum += p;
+    }
+    sum = reduce(sum, true);
+    if (tid < MQ) {
+      f_s[tid] = exp2f(old - ref);
+      m_s[tid] = now;
+      l_s[tid] = l_s[tid] * f_s[tid] + sum;
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMergeQ; ++i) {
-      const float now = fmaxf(m[i], fmaxf(fmaxf(red_s[0][i], red_s[1][i]), fmaxf(red_s[2][i], red_s[3][i])));
-      const float ref = now == -INFINITY ? 0.f : now;
-      const float f = exp2f(m[i] - ref);
-      l[i] *= f;
-      o[i] *= f;
-      m[i] = now;
-      if (!half) {
-        const bool on = key < nk && ((vis_s[i][(j0 + key) >> 6] >> ((j0 + key) & 63)) & 1);
-        s[i] = on ? exp2f(s[i] - ref) : 0.f;   // a NaN score stays
-        p_s[key][i] = s[i];
-      }
-    }
-    __syncthreads();
-    if (!half) {
-#pragma unroll
-      for (int i = 0; i < kMergeQ; ++i) {
-        float v = s[i];
-#pragma unroll
-        for (int f = 16; f > 0; f >>= 1) v += __shfl_xor_sync(0xffffffffu, v, f);
-        if (lane == 0) red_s[warp][i] = v;
-      }
-    }
     if (ch < D) {
+#pragma unroll
+      for (int i = 0; i < MQ; ++i) o[i] *= f_s[i];
+#pragma unroll 2
       for (int k = half; k < nk; k += 2) {
         const float v = bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(kv_s + k * kDraftPitch + ch * 2));
-        const float4 x = *reinterpret_cast<const float4*>(p_s[k]), y = *reinterpret_cast<const float4*>(p_s[k] + 4);
-        const float pk[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        if (isfinite(v)) {
+        const float4* pp = reinterpret_cast<const float4*>(p_s[k]);
+        if (__builtin_expect(isfinite(v), 1)) {
 #pragma unroll
-          for (int i = 0; i < kMergeQ; ++i) o[i] = fmaf(pk[i], v, o[i]);
+          for (int i = 0; i < MQ / 4; ++i) {
+            const float4 x = pp[i];
+            o[4 * i] = fmaf(x.x, v, o[4 * i]);
+            o[4 * i + 1] = fmaf(x.y, v, o[4 * i + 1]);
+            o[4 * i + 2] = fmaf(x.z, v, o[4 * i + 2]);
+            o[4 * i + 3] = fmaf(x.w, v, o[4 * i + 3]);
+          }
         } else {   // enters only where it is seen
 #pragma unroll
-          for (int i = 0; i < kMergeQ; ++i)
-            if ((vis_s[i][(j0 + k) >> 6] >> ((j0 + k) & 63)) & 1) o[i] = fmaf(pk[i], v, o[i]);
+          for (int i = 0; i < MQ; ++i)
+            if ((vis_s[i][(j0 + k) >> 6] >> ((j0 + k) & 63)) & 1) o[i] = fmaf(p_s[k][i], v, o[i]);
         }
       }
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMergeQ; ++i) l[i] += (red_s[0][i] + red_s[1][i]) + (red_s[2][i] + red_s[3][i]);
   }
 
   // the cached tokens' partial states: the lower half takes the anchor's part, the upper the residual's
   pdl_wait();
   __syncthreads();
-  const int c_lo = range_s[0], c_hi = range_s[1];
-  const int unit = bh * a.nqb + r0 / NB, qo = r0 % NB;
-  const float* part = a.partials + (size_t)unit * a.pstride;
-  float ref[kMergeQ];      // common reference
+  const int c_lo = range_s[0], c_hi = range_s[1], qo = r0 % NB;
+  const float* unit = a.partials + (size_t)(bh * a.nqb + r0 / NB) * a.pstride;
+  float mx = -INFINITY;
+  for (int c = c_lo + part; c <= c_hi; c += PARTS) mx = fmaxf(mx, __ldcg(unit + (size_t)c * a.pstride + qo + my_q));
+  const float old = m_s[my_q];
+  float ref = fmaxf(old, reduce(mx, false));     // common reference
+  if (ref == -INFINITY) ref = 0.f;
+  const float fd = exp2f(old - ref);             // the draft's weight
+  float oc[MQ], lsum = 0.f;                      // this thread's plane of the cached tokens; their sums
 #pragma unroll
-  for (int i = 0; i < kMergeQ; ++i) ref[i] = m[i];
-#pragma unroll 4
-  for (int c = c_lo; c <= c_hi; ++c) {
-    const float4* mp = reinterpret_cast<const float4*>(part + (size_t)c * a.pstride + qo);
-    const float4 x = __ldcg(mp), y = __ldcg(mp + 1);
-    ref[0] = fmaxf(ref[0], x.x); ref[1] = fmaxf(ref[1], x.y); ref[2] = fmaxf(ref[2], x.z); ref[3] = fmaxf(ref[3], x.w);
-    ref[4] = fmaxf(ref[4], y.x); ref[5] = fmaxf(ref[5], y.y); ref[6] = fmaxf(ref[6], y.z); ref[7] = fmaxf(ref[7], y.w);
-  }
-  float oc[kMergeQ];       // this thread's plane of the cached tokens
-#pragma unroll
-  for (int i = 0; i < kMergeQ; ++i) {
-    if (ref[i] == -INFINITY) ref[i] = 0.f;
-    const float f = exp2f(m[i] - ref[i]);
-    l[i] *= f;
-    o[i] *= f;
-    oc[i] = 0.f;
-  }
+  for (int i = 0; i < MQ; ++i) oc[i] = 0.f;
   const bool mine = ch < D && (NRES || !half);
-#pragma unroll 2
-  for (int c = c_lo; c <= c_hi; ++c) {
-    const float* p = part + (size_t)c * a.pstride;
-    const float4 m0 = __ldcg(reinterpret_cast<const float4*>(p + qo)), m1 = __ldcg(reinterpret_cast<const float4*>(p + qo) + 1);
-    const float4 l0 = __ldcg(reinterpret_cast<const float4*>(p + NB + qo)),
-                 l1 = __ldcg(reinterpret_cast<const float4*>(p + NB + qo) + 1);
-    float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
+#pragma unroll 1
+  for (int c0 = c_lo; c0 <= c_hi; c0 += kMergeChunk) {
+    const int nc = min(kMergeChunk, c_hi - c0 + 1);
+    if (c0 != c_lo) __syncthreads();
+    for (int c = part; c < nc; c += PARTS) {
+      const float* p = unit + (size_t)(c0 + c) * a.pstride + qo + my_q;
+      const float w = exp2f(__ldcg(p) - ref);
+      w_s[c][my_q] = w;
+      lsum = fmaf(w, __ldcg(p + NB), lsum);
+    }
+    __syncthreads();
     if (mine) {
-      const float4* xp = reinterpret_cast<const float4*>(p + 2 * NB) + (size_t)(half * (NB / 4) + qo / 4) * D + ch;
-      x0 = __ldcg(xp);
-      x1 = __ldcg(xp + D);
-    }
-    const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
-    const float ll[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
-    const float xx[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll 4
+      for (int c = 0; c < nc; ++c) {
+        const float4* xp = reinterpret_cast<const float4*>(unit + (size_t)(c0 + c) * a.pstride + 2 * NB) +
+                           (size_t)(half * (NB / 4) + qo / 4) * D + ch;
+        const float4* wp = reinterpret_cast<const float4*>(w_s[c]);
 #pragma unroll
-    for (int i = 0; i < kMergeQ; ++i) {
-      const float f = exp2f(mm[i] - ref[i]);
-      l[i] = fmaf(f, ll[i], l[i]);
-      oc[i] = fmaf(f, xx[i], oc[i]);
-    }
-  }
-  // the operands' powers of two: V's anchor under a coefficient 2^-7, else 2^-15
-  const float up = NRES && !half ? 128.f : 32768.f;
-#pragma unroll
-  for (int i = 0; i < kMergeQ; ++i) oc[i] *= up;
-  if (!half) {
-#pragma unroll
-    for (int i = 0; i < kMergeQ; ++i) o[i] += oc[i];
-  }
-  if (NRES && c_hi >= c_lo) {   // R^T: a thread sums half of the channels for one output channel
-    if ((a.g.mode & RQ_MODE_HADAMARD) != 0) {
-      if (half) {
-#pragma unroll
-        for (int i = 0; i < kMergeQ; ++i) p_s[ch][i] = oc[i];
-      }
-      __syncthreads();
-      float t[kMergeQ];
-#pragma unroll
-      for (int i = 0; i < kMergeQ; ++i) t[i] = half ? 0.f : p_s[ch][i];
-      __syncthreads();
-      hadamard128<kMergeQ>(t, tid, &q_s[0][0]);   // threads >= 128 only take part in its barriers
-      if (!half) {
-#pragma unroll
-        for (int i = 0; i < kMergeQ; ++i) o[i] += t[i];
-      }
-    } else {
-      if (half) {
-#pragma unroll
-        for (int i = 0; i < kMergeQ; ++i) p_s[ch][i] = oc[i];
-      }
-      __syncthreads();
-      if (ch < D) {
-#pragma unroll 16
-        for (int k = half * (D / 2); k < (half + 1) * (D / 2); ++k) {
-          const float r = __ldg(a.R + (size_t)k * D + ch);
-          const float4 x = *reinterpret_cast<const float4*>(p_s[k]), y = *reinterpret_cast<const float4*>(p_s[k] + 4);
-          o[0] = fmaf(r, x.x, o[0]); o[1] = fmaf(r, x.y, o[1]); o[2] = fmaf(r, x.z, o[2]); o[3] = fmaf(r, x.w, o[3]);
-          o[4] = fmaf(r, y.x, o[4]); o[5] = fmaf(r, y.y, o[5]); o[6] = fmaf(r, y.z, o[6]); o[7] = fmaf(r, y.w, o[7]);
+        for (int i = 0; i < MQ / 4; ++i) {
+          const float4 x = __ldcg(xp + i * D), w = wp[i];
+          oc[4 * i] = fmaf(w.x, x.x, oc[4 * i]);
+          oc[4 * i + 1] = fmaf(w.y, x.y, oc[4 * i + 1]);
+          oc[4 * i + 2] = fmaf(w.z, x.z, oc[4 * i + 2]);
+          oc[4 * i + 3] = fmaf(w.w, x.w, oc[4 * i + 3]);
         }
       }
     }
   }
+  lsum = reduce(lsum, true);                     // its barriers also free p_s
+  if (tid < MQ) {
+    l_s[tid] = l_s[tid] * fd + lsum;
+    f_s[tid] = fd;
+  }
+  // the operands' powers of two: V's anchor under a coefficient 2^-7, else 2^-15
+  const float up = NRES && !half ? 128.f : 32768.f;
+#pragma unroll
+  for (int i = 0; i < MQ; ++i) oc[i] *= up;
+  if (NRES && half) {
+#pragma unroll
+    for (int i = 0; i < MQ; ++i) p_s[ch][i] = oc[i];
+  }
   __syncthreads();
+#pragma unroll
+  for (int i = 0; i < MQ; ++i) o[i] = o[i] * f_s[i] + (half ? 0.f : oc[i]);
+  float* h_s = reinterpret_cast<float*>(kv_s);   // [query][channel + pad]: what joins the lower half's sum
+  constexpr int HP = 132;
+  if (NRES && hadamard) {
+    float t[MQ];
+#pragma unroll
+    for (int i = 0; i < MQ; ++i) t[i] = half ? 0.f : p_s[ch][i];
+    __syncthreads();
+    hadamard128<MQ>(t, tid, h_s);   // threads >= 128 only take part in its barriers
+    __syncthreads();
+    if (!half) {
+#pragma unroll
+      for (int i = 0; i < MQ; ++i) o[i] += t[i];
+    }
+  }
   if (half) {
 #pragma unroll
-    for (int i = 0; i < kMergeQ; ++i) h_s[ch][i] = o[i];
+    for (int i = 0; i < MQ; ++i) h_s[i * HP + ch] = o[i];
+  }
+  __syncthreads();
+  if (dense) {
+    float d[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        uint32_t bh2[2], bl2[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int kk = 16 * k + 2 * t4 + 8 * i;
+          bf16_pieces(make_float2(p_s[kk][8 * n + g], p_s[kk + 1][8 * n + g]), bh2[i], bl2[i]);
+        }
+        mma_bf16(d[n], rhi[k], bh2[0], bh2[1]);
+        mma_bf16(d[n], rlo[k], bh2[0], bh2[1]);
+        mma_bf16(d[n], rhi[k], bl2[0], bl2[1]);
+      }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float* h = h_s + (8 * n + 2 * t4) * HP + 16 * warp + g;
+      h[0] += d[n][0];
+      h[HP] += d[n][1];
+      h[8] += d[n][2];
+      h[HP + 8] += d[n][3];
+    }
   }
   __syncthreads();
   if (!half && ch < D) {
     __nv_bfloat16* op = a.out + ((size_t)bh * a.M + r0) * D + ch;
 #pragma unroll
-    for (int i = 0; i < kMergeQ; ++i)
+    for (int i = 0; i < MQ; ++i) {
+      const float l = l_s[i];
       if (i < nq && (r0 + i) % a.T < cnt)   // no key seen: zero; NaN stays
-        op[(size_t)i * D] = __float2bfloat16_rn(l[i] != 0.f ? (o[i] + h_s[ch][i]) / l[i] : 0.f);
+        op[(size_t)i * D] = __float2bfloat16_rn(l != 0.f ? (o[i] + h_s[i * HP + ch]) / l : 0.f);
+    }
   }
 }
 
@@ -1432,8 +1462,14 @@ cudaError_t launch_tree_t(const TreeArgs& args, int num_sms, cudaStream_t stream
   if (e != cudaSuccess) return e;
   e = launch_dependent(kern, dim3(num_sms), dim3(kTreeThreads), (size_t)C::SMEM, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_dependent(tree_merge_kernel<D, NRES, NB>, dim3(a.batch * a.g.H * ((a.M + kMergeQ - 1) / kMergeQ)),
-                          dim3(kMergeThreads), 0, stream, a, num_sms);
+  // queries a merge CTA: 8, or 16 once that still leaves every SM several CTAs (R^T and the draft are
+  // then read half as often)
+  const int bh = a.batch * a.g.H;
+  if (bh * ((a.M + 15) / 16) >= 2 * num_sms)
+    return launch_dependent(tree_merge_kernel<D, NRES, NB, 16>, dim3(bh * ((a.M + 15) / 16)), dim3(kMergeThreads), 0,
+                            stream, a, num_sms);
+  return launch_dependent(tree_merge_kernel<D, NRES, NB, 8>, dim3(bh * ((a.M + 7) / 8)), dim3(kMergeThreads), 0, stream,
+                          a, num_sms);
 }
 
 template <int D, int GS, int NRES>
