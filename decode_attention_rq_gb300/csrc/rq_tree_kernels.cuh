@@ -14,9 +14,9 @@
 //   values  O^T [channels x NB] += V'^T P^T     (anchor and residual part apart)
 // K' and V'^T are dequantized into registers and stored to tensor memory as the A operand
 // (f16, one token or channel per lane): dequantized data never touches shared memory.
-// Roles (24 warps, in groups of four, one per 32 lanes): K, softmax, two for V of the anchor, V of
-// the residual (idle in the anchor loop), and a group with the copy warp and one warp for each
-// kind of product.
+// Roles (24 warps, in groups of four, one per 32 lanes): K, softmax, two for V of the anchor (64
+// queries: one, and a second for softmax, 32 queries each), V of the residual (idle in the anchor
+// loop), and a group with the copy warp and one warp for each kind of product.
 //
 // Dequantization: an f16 whose bits are an integer n < 1024 has the value n 2^-24, so masking a
 // code word leaves codes times 2^(p - 24), p the field's first bit; one fused multiply-add with
@@ -341,17 +341,19 @@ struct TreeCfg {
   static constexpr int SCOLS = 2 * NB;                     // Sa, Sr
   static_assert(S0 + SCOLS <= 512, "tensor memory");
   static_assert(SMEM <= 227 * 1024 - 5120, "shared memory");
-  // registers a thread: 80 at launch (6 groups: 480), then softmax, the four dequantizers, copies
-  static constexpr int REGS = NB == 64 ? 176 : 136;
-  static constexpr int REGD = NB == 64 ? 64 : 72;
-  static constexpr int REGP = NB == 64 ? 48 : 56;
-  static_assert(REGS + 4 * REGD + REGP <= 480, "registers");
+  static constexpr int NS = NB / 32 > 1 ? 2 : 1, NQ = NB / NS;   // softmax groups, queries of each
+  static constexpr int NVA = 3 - NS;                             // groups of V's anchor
+  // registers a thread: 80 at launch (6 groups: 480), then softmax, the dequantizers, the others
+  static constexpr int REGS = NS == 2 ? 112 : 136;
+  static constexpr int REGD = NS == 2 ? 64 : 72;
+  static constexpr int REGP = 56;
+  static_assert(NS * REGS + (5 - NS) * REGD + REGP <= 480, "registers");
   // floats of a partial: m[NB], l[NB], O as [plane][NB/4][D][4]
   static constexpr int PSTRIDE = 2 * NB + PL * NB * D;
 };
 
 // ---- query prep --------------------------------------------------------------------
-// One CTA per unit: x and R x as f16 times a power of two of the query's own (its largest
+// One CTA per 16 queries of a unit: x and R x as f16 times a power of two of the query's own (its largest
 // component to 2^10 .. 2^11: R keeps norms, so both stay below 2^15), in the layout of the B
 // operand.  x is BF16 and so exact; R x is a product on the 16-bit tensor cores with R as two
 // BF16 pieces (16 bits, against the 11 of its result), summed in float32: 8 warps with 16 rows
@@ -376,11 +378,12 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
   constexpr int IMG = PL * (D / 16) * NB * 32;
   constexpr int PITCH = D + 8;             // BF16 elements: rows 4 banks apart
   constexpr int RPITCH = D + 4;
-  __shared__ __align__(16) __nv_bfloat16 q_s[NB][PITCH];
-  __shared__ __align__(16) float r_s[NRES ? NB : 1][RPITCH];
-  __shared__ float up_s[NB];               // the query's power of two
+  constexpr int QP = 16;                   // queries of this CTA
+  __shared__ __align__(16) __nv_bfloat16 q_s[QP][PITCH];
+  __shared__ __align__(16) float r_s[NRES ? QP : 1][RPITCH];
+  __shared__ float up_s[QP];               // the query's power of two
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  const int unit = blockIdx.x, qb = unit % a.nqb, bh = unit / a.nqb, b = bh / a.g.H;
+  const int unit = blockIdx.x / (NB / QP), q0 = blockIdx.x % (NB / QP) * QP, qb = unit % a.nqb, bh = unit / a.nqb, b = bh / a.g.H;
   const bool hadamard = (a.g.mode & RQ_MODE_HADAMARD) != 0;
   uint32_t hi[NRES ? D / 16 : 1][4], lo[NRES ? D / 16 : 1][4];
   if (NRES && !hadamard && warp < D / 16) {   // R does not change while the cache is used: before the wait
@@ -394,13 +397,13 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
   pdl_wait();
   pdl_launch_dependents();   // what ran before the call is complete: the next kernel may read the cache
   const int cnt = a.counts ? clamp_len(a.counts[b], a.T) : a.T;
-  const __nv_bfloat16* qu = a.q + ((size_t)bh * a.M + (size_t)qb * NB) * D;
-  const int rows = min(NB, a.M - qb * NB);
+  const int at = qb * NB + q0, rows = min(QP, a.M - at);   // may be negative: no query here
+  const __nv_bfloat16* qu = a.q + ((size_t)bh * a.M + at) * D;
   // one warp per query: its values (zeros for a node not in use), its power of two; a query that
   // is not finite keeps the scale 1 and stays so
-#pragma unroll 4
-  for (int r = warp; r < NB; r += 8) {
-    const bool on = r < rows && (qb * NB + r) % a.T < cnt;
+#pragma unroll
+  for (int r = warp; r < QP; r += 8) {
+    const bool on = r < rows && (at + r) % a.T < cnt;
     uint2 v = make_uint2(0u, 0u);
     if (on && lane < D / 4) v = __ldg(reinterpret_cast<const uint2*>(qu + (size_t)r * D) + lane);
     if (lane < D / 4) *reinterpret_cast<uint2*>(&q_s[r][4 * lane]) = v;
@@ -412,13 +415,13 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
     e = max(e, -115);                                                       // 2^(11 - e) stays finite
     if (lane == 0) {
       up_s[r] = ldexpf(1.f, 11 - e);
-      a.q_scale[(size_t)unit * NB + r] = ldexpf(a.qscale, e - 11 + kScaleK);
+      a.q_scale[(size_t)unit * NB + q0 + r] = ldexpf(a.qscale, e - 11 + kScaleK);
     }
   }
   __syncthreads();
   if (NRES && hadamard) {
     // one warp per query: lane holds channels lane, lane + 32, ...; stages h = 1 .. 64
-    for (int r = warp; r < NB; r += 8) {
+    for (int r = warp; r < QP; r += 8) {
       float v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = __bfloat162float(q_s[r][(lane + 32 * i) % D]);
@@ -440,8 +443,8 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
     __syncthreads();
   } else if (NRES) {
     if (warp < D / 16) {
-#pragma unroll 2
-      for (int n = 0; n < NB; n += 8) {
+#pragma unroll
+      for (int n = 0; n < QP; n += 8) {
         float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -461,8 +464,8 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
   }
   // the operand: 8 channels (16 bytes) a thread, 16 to a block of 32 bytes a query, swizzled
   uint8_t* img = a.packs + (size_t)unit * IMG;
-  for (int i = tid; i < PL * NB * (D / 8); i += 256) {
-    const int c = i % (D / 8), r = i / (D / 8) % NB, pl = i / (D / 8 * NB);
+  for (int i = tid; i < PL * QP * (D / 8); i += 256) {
+    const int c = i % (D / 8), r = i / (D / 8) % QP, pl = i / (D / 8 * QP), row = q0 + r;
     const float up = up_s[r];
     uint32_t w[4];
 #pragma unroll
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
       const float x1 = pl ? r_s[NRES ? r : 0][ch + 8] : __bfloat162float(q_s[r][ch + 4]);
       w[j] = f16x2(x0 * up, x1 * up);
     }
-    *reinterpret_cast<uint4*>(img + ((pl * (D / 16) + (c >> 1)) * NB + r) * 32 + (((c & 1) ^ ((r >> 2) & 1)) << 4)) =
+    *reinterpret_cast<uint4*>(img + ((pl * (D / 16) + (c >> 1)) * NB + row) * 32 + (((c & 1) ^ ((row >> 2) & 1)) << 4)) =
         make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
@@ -505,14 +508,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
 
   tree_rows(a, &rows_s);
   if (tid == 32) {
-    for (int i = 0; i < ST; ++i) { mbar_init(&full_bar[i], 1); mbar_init(&empty_bar[i], NRES ? 20 : 12); }
+    for (int i = 0; i < ST; ++i) { mbar_init(&full_bar[i], 1); mbar_init(&empty_bar[i], NRES ? 20 : 4 + 4 * C::NVA); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull_bar[i], 1); mbar_init(&qempty_bar[i], 1);
       mbar_init(&kfull_bar[i], 4); mbar_init(&kempty_bar[i], 1);
-      mbar_init(&vfull_bar[i], i ? 4 : 8); mbar_init(&vempty_bar[i], 1);
+      mbar_init(&vfull_bar[i], i ? 4 : 4 * C::NVA); mbar_init(&vempty_bar[i], 1);
     }
-    mbar_init(&sfull_bar, 1); mbar_init(&sempty_bar, 4);
-    mbar_init(&pfull_bar, 4); mbar_init(&pempty_bar, 1);
+    mbar_init(&sfull_bar, 1); mbar_init(&sempty_bar, 4 * C::NS);
+    mbar_init(&pfull_bar, 4 * C::NS); mbar_init(&pempty_bar, 1);
     mbar_init(&drain_bar[0], 1); mbar_init(&drain_bar[1], 1);
     fence_mbar_init();
   }
@@ -554,7 +557,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
   auto v_role = [&](auto plane, int part) {
     constexpr int pl = decltype(plane)::value;
     const int w4 = warp & 3, lt = tid & 127;
-    auto v_sync = [&]() { if (pl) wg_sync(3); else wg_sync2(2); };   // the groups that share constants
+    auto v_sync = [&]() { if (pl) wg_sync(3); else if (C::NVA == 1) wg_sync(2); else wg_sync2(2); };   // the groups that share constants
     const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
     const int col = v_slot(lt) >> 1, hf = v_slot(lt) & 1;   // the token's place among the constants
     const int t4 = lane & 3;                                // the lane's 32 tokens: 32 t4 ..
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + (pl ? C::R_CODES : C::A_CODES)) + tok * NG;
 #pragma unroll
         for (int gi = 0; gi < NG; ++gi) {
-          if (pl == 0 && (gi & 1) != part) continue;
+          if (pl == 0 && C::NVA == 2 && (gi & 1) != part) continue;
           __half2 so = __hmul2(e4m3_pair(on ? meta[gi] : (uint16_t)0), to_k);
           if (pl) so = __hmul2(so, field);
           else if (NRES) so = __hmul2(__hmul2(so, f1), f2);
@@ -625,7 +628,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
               if (NRES && pl == 0) mq[j] = cm[16 * c + 4 * j];
             }
 #pragma unroll 1
-            for (int hh = pl ? 0 : part; hh < (pl ? 2 : part + 1); ++hh) {
+            for (int hh = pl || C::NVA == 1 ? 0 : part; hh < (pl || C::NVA == 1 ? 2 : part + 1); ++hh) {
               if (GS == 16) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) kq[j] = tb[hh * 32 + 16 * c + 4 * j];
@@ -806,14 +809,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     wait(&drain_bar[1], 0);
     __syncwarp();
   }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >> 2 == 1 || (C::NS == 2 && warp >> 2 == 3)) {
     reg_inc<C::REGS>();
     // ================= softmax: one token a lane =================
-    const int lt = tid - 128, tok = lt & 63, tau = lt >> 6, w4 = warp - 4;
+    const int lt = tid & 127, tok = lt & 63, tau = lt >> 6, w4 = warp & 3;
+    // this group's queries: NQ from q_at; its named barrier
+    constexpr int NQ = C::NQ;
+    const int q_at = C::NS == 2 && warp >= 12 ? NQ : 0, my_bar = q_at ? 4 : 1;
+    float(*qm)[4] = qm_s + q_at / 2;
+    float* f_q = f_s + q_at;
     const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
     const int slot = v_slot(lt);
-    constexpr bool KEEP = NB <= 32;
-    float l[NB];
+    float l[NQ];
     pdl_wait();
     int st = 0;
     uint32_t par = 0;
@@ -825,12 +832,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       const int unit = info.y;
       if (first) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i) l[i] = 0.f;
-        if (lt < NB) {
-          qm_s[lt >> 1][lt & 1] = __ldcg(a.q_scale + (size_t)unit * NB + lt);
-          qm_s[lt >> 1][2 + (lt & 1)] = INFINITY;
+        for (int i = 0; i < NQ; ++i) l[i] = 0.f;
+        if (lt < NQ) {
+          qm[lt >> 1][lt & 1] = __ldcg(a.q_scale + (size_t)unit * NB + q_at + lt);
+          qm[lt >> 1][2 + (lt & 1)] = INFINITY;
         }
-        wg_sync(1);
+        wg_sync(my_bar);
       }
       float c = 0.f;
       if (NRES) {
@@ -844,7 +851,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       }
       const float2 c2 = make_float2(c, c);
       tc_after();
-      const uint32_t s0 = lanes + C::S0;
+      const uint32_t s0 = lanes + C::S0 + q_at;
       // score products of 16 queries with this lane's token
       auto scores = [&](int ch, float2 (&y)[8]) {
         uint32_t ra[16], rr[16];
@@ -862,91 +869,86 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       auto relative = [&](int ch, float2 (&y)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float4 k = *reinterpret_cast<const float4*>(qm_s[8 * ch + i]);
+          const float4 k = *reinterpret_cast<const float4*>(qm[8 * ch + i]);
           y[i] = fma2(y[i], make_float2(k.x, k.y), make_float2(k.z, k.w));
         }
       };
       float top = -INFINITY;
-      float2 kept[KEEP ? NB / 2 : 1];     // relative scores, where they fit the registers
+      float2 kept[NQ / 2];     // relative scores
 #pragma unroll
-      for (int ch = 0; ch < NB / 16; ++ch) {
+      for (int ch = 0; ch < NQ / 16; ++ch) {
         float2 y[8];
         scores(ch, y);
         relative(ch, y);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           top = fmaxf(top, fmaxf(y[i].x, y[i].y));
-          if (KEEP) kept[(KEEP ? 8 * ch + i : 0)] = y[i];
+          kept[8 * ch + i] = y[i];
         }
       }
-      if (__builtin_expect(wg_any(1, on && top > kTop), 0)) {
+      if (__builtin_expect(wg_any(my_bar, on && top > kTop), 0)) {
         // move the references to this step's maxima where those are higher
 #pragma unroll
-        for (int ch = 0; ch < NB / 16; ++ch) {
+        for (int ch = 0; ch < NQ / 16; ++ch) {
           float2 y[8];
           scores(ch, y);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            float v = on ? (i & 1 ? y[i / 2].y : y[i / 2].x) * qm_s[8 * ch + i / 2][i & 1] : -INFINITY;
+            float v = on ? (i & 1 ? y[i / 2].y : y[i / 2].x) * qm[8 * ch + i / 2][i & 1] : -INFINITY;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-            if (lane == 0) wred_s[w4][16 * ch + i] = v;
+            if (lane == 0) wred_s[w4][q_at + 16 * ch + i] = v;
           }
         }
-        wg_sync(1);
-        if (lt < NB) {
-          const float old = -qm_s[lt >> 1][2 + (lt & 1)];
-          const float mx = fmaxf(fmaxf(wred_s[0][lt], wred_s[1][lt]), fmaxf(wred_s[2][lt], wred_s[3][lt])) - kHead;
+        wg_sync(my_bar);
+        if (lt < NQ) {
+          const float old = -qm[lt >> 1][2 + (lt & 1)];
+          const float(*wr)[NB] = wred_s;
+          const int q = q_at + lt;
+          const float mx = fmaxf(fmaxf(wr[0][q], wr[1][q]), fmaxf(wr[2][q], wr[3][q])) - kHead;
           const float now = fmaxf(old, mx);
-          f_s[lt] = old == now ? 1.f : exp2f(old - now);
-          qm_s[lt >> 1][2 + (lt & 1)] = -now;
+          f_q[lt] = old == now ? 1.f : exp2f(old - now);
+          qm[lt >> 1][2 + (lt & 1)] = -now;
         }
-        wg_sync(1);
+        wg_sync(my_bar);
 #pragma unroll
-        for (int i = 0; i < NB; ++i) l[i] *= f_s[i];
+        for (int i = 0; i < NQ; ++i) l[i] *= f_q[i];
         if (!first) {   // O holds products of the steps before: all of them done, then scaled
           wait_warp(&pempty_bar, (it - 1) & 1);
           tc_after();
 #pragma unroll
-          for (int ch = 0; ch < PL * NB / 16; ++ch) {
+          for (int ch = 0; ch < PL * NQ / 16; ++ch) {
             uint32_t r[16];
-            tc_ld16(lanes + C::OA + 16 * ch, r);
+            const uint32_t at = lanes + C::OA + (16 * ch / NQ) * NB + q_at + 16 * ch % NQ;
+            tc_ld16(at, r);
             tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f_s[(16 * ch + i) % NB]);
-            tc_st16(lanes + C::OA + 16 * ch, r);
+            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f_q[(16 * ch + i) % NQ]);
+            tc_st16(at, r);
           }
           tc_wait_st();
         }
-        if (KEEP) {
 #pragma unroll
-          for (int ch = 0; ch < NB / 16; ++ch) {
-            float2 y[8];
-            scores(ch, y);
-            relative(ch, y);
+        for (int ch = 0; ch < NQ / 16; ++ch) {
+          float2 y[8];
+          scores(ch, y);
+          relative(ch, y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) kept[(KEEP ? 8 * ch + i : 0)] = y[i];
-          }
+          for (int i = 0; i < 8; ++i) kept[8 * ch + i] = y[i];
         }
       }
       // weights
-      if (KEEP) {   // the scores are in registers: their place in tensor memory is free
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sempty_bar);
-      }
+      // the scores are in registers: their place in tensor memory is free
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sempty_bar);
       wait_warp(&pempty_bar, (it & 1) ^ 1);
       uint8_t* prow = p_buf + slot * 128;
 #pragma unroll
-      for (int ch = 0; ch < NB / 16; ++ch) {
+      for (int ch = 0; ch < NQ / 16; ++ch) {
         float2 y[8];
-        if (KEEP) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = kept[(KEEP ? 8 * ch + i : 0)];
-        } else {
-          scores(ch, y);
-          relative(ch, y);
-        }
+        for (int i = 0; i < 8; ++i) y[i] = kept[8 * ch + i];
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -956,16 +958,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
           l[16 * ch + 2 * i + 1] += y[i].y;
           w[i] = f16x2(y[i].x, y[i].y);
         }
-        *reinterpret_cast<uint4*>(prow + (((2 * ch) ^ (slot & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(prow + (((2 * ch + 1) ^ (slot & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+        *reinterpret_cast<uint4*>(prow + (((q_at / 8 + 2 * ch) ^ (slot & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(prow + (((q_at / 8 + 2 * ch + 1) ^ (slot & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
       }
       fence_async_smem();
       tc_before();
       __syncwarp();
-      if (lane == 0) {
-        if (!KEEP) mbar_arrive(&sempty_bar);
-        mbar_arrive(&pfull_bar);
-      }
+      if (lane == 0) mbar_arrive(&pfull_bar);
       if (__builtin_expect((info.x & 512) != 0, 0)) {
         // the unit's state out
         wait_warp(&pempty_bar, it & 1);
@@ -973,26 +972,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         float* part = a.partials + (size_t)(blockIdx.x + unit) * a.pstride;
         if (lt < D) {
 #pragma unroll
-          for (int c = 0; c < PL * NB / 16; ++c) {
+          for (int c = 0; c < PL * NQ / 16; ++c) {
             uint32_t r[16];
+            const int q0 = (16 * c / NQ) * NB + q_at + 16 * c % NQ;   // plane and query
             if (D == 128 || w4 < 3) {
-              tc_ld16(lanes + C::OA + 16 * c, r);
+              tc_ld16(lanes + C::OA + q0, r);
               tc_wait_ld();
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(part + 2 * NB + ((size_t)(4 * c + i) * D + lt) * 4) =
+              *reinterpret_cast<uint4*>(part + 2 * NB + ((size_t)(q0 / 4 + i) * D + lt) * 4) =
                   make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
           }
         }
         tc_before();
         // sums over the lanes: reduce-scatter, then over the warps in order
 #pragma unroll
-        for (int o = 16, n = NB / 2; o >= 1; o >>= 1) {
+        for (int o = 16, n = NQ / 2; o >= 1; o >>= 1) {
           if (n >= 1) {
             const bool up = (lane & o) != 0;
 #pragma unroll
-            for (int i = 0; i < (NB >= 32 ? NB / 2 : 8); ++i)
+            for (int i = 0; i < NQ / 2; ++i)
               if (i < n) {
                 const float send = up ? l[i] : l[i + n], keep = up ? l[i + n] : l[i];
                 l[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
@@ -1002,21 +1002,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
             l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
           }
         }
-        // NB = 64: lane holds queries q0, q0 + 1 ...: the bits of the lane, highest first
-        if (NB == 64) {
-          wred_s[w4][lane * 2] = l[0];
-          wred_s[w4][lane * 2 + 1] = l[1];
-        } else if (NB == 32) {
-          wred_s[w4][lane] = l[0];
-        } else if ((lane & 1) == 0) {
+        // 32 queries: one a lane; 16: one for two lanes
+        if (NQ == 32)
+          wred_s[w4][q_at + lane] = l[0];
+        else if ((lane & 1) == 0)
           wred_s[w4][lane >> 1] = l[0];
+        wg_sync(my_bar);
+        if (lt < NQ) {
+          const int q = q_at + lt;
+          part[q] = -qm[lt >> 1][2 + (lt & 1)];
+          part[NB + q] = wred_s[0][q] + wred_s[1][q] + wred_s[2][q] + wred_s[3][q];
         }
-        wg_sync(1);
-        if (lt < NB) {
-          part[lt] = -qm_s[lt >> 1][2 + (lt & 1)];
-          part[NB + lt] = wred_s[0][lt] + wred_s[1][lt] + wred_s[2][lt] + wred_s[3][lt];
-        }
-        wg_sync(1);
+        wg_sync(my_bar);
       }
     }
   } else {
@@ -1142,7 +1139,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       if (lane == 0) mbar_arrive(&empty_bar[st]);
       if (++st == ST) { st = 0; par ^= 1; }
     }
-    } else if (warp < 16) {
+    } else if (warp < 16) {   // 8 .. 11; with one softmax group 12 .. 15, too
       v_role(std::integral_constant<int, 0>{}, warp >= 12);
     } else if (NRES) {
       v_role(std::integral_constant<int, NRES>{}, 0);
@@ -1458,7 +1455,7 @@ cudaError_t launch_tree_t(const TreeArgs& args, int num_sms, cudaStream_t stream
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const int units = a.batch * a.g.H * a.nqb;
-  e = launch_dependent(tree_prep_kernel<D, NRES, NB>, dim3(units), dim3(256), 0, stream, a);
+  e = launch_dependent(tree_prep_kernel<D, NRES, NB>, dim3(units * (NB / 16)), dim3(256), 0, stream, a);
   if (e != cudaSuccess) return e;
   e = launch_dependent(kern, dim3(num_sms), dim3(kTreeThreads), (size_t)C::SMEM, stream, a);
   if (e != cudaSuccess) return e;
