@@ -236,21 +236,35 @@ def rq_decode_attention_bf16(k_cache, v_cache, k_cur, v_cur, q, seq_lens, batch,
         _stream(stream)))
 
 
-def _arg(fn, x, dtypes, count=None):
+def _setup():
+    """torch and what the argument checks below compare with, once: a call of a
+    few microseconds on the device should not wait for its marshalling."""
+    global _torch, _DT, _ROPE_DT
+    import torch
+    _DT = {"i32": (torch.int32,), "bf16": (torch.bfloat16,), "u64": (torch.int64, torch.uint64), "u8": (torch.uint8,)}
+    _ROPE_DT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    _torch = torch
+
+
+_torch = None
+
+
+def _device():
+    if _torch is None:
+        _setup()
+    return _torch.cuda.current_device()
+
+
+def _arg(fn, dev, x, kind, count=0):
     """Address of x for a C call.  None and ints (device addresses) pass as they
-    are; a tensor has to be contiguous, of one of the dtypes (names), on the
-    device current on this thread and, where count is given, that long: a host
-    pointer or a short buffer would fault the device."""
+    are; a tensor has to be contiguous, of the kind's dtype, on device dev (the one
+    current on this thread) and at least `count` long: a host pointer or a short
+    buffer would fault the device."""
     if x is None or isinstance(x, int):
         return x
-    import torch
-    if (not x.is_cuda or str(x.dtype).split(".")[1] not in dtypes or not x.is_contiguous()
-            or x.device.index != torch.cuda.current_device() or (count is not None and x.numel() < count)):
+    if x.dtype not in _DT[kind] or x.get_device() != dev or x.numel() < count or not x.is_contiguous():
         raise RqError(fn, 1)
     return x.data_ptr()
-
-
-_I32, _BF16, _U64, _U8 = ("int32",), ("bfloat16",), ("int64", "uint64"), ("uint8",)
 
 
 def rq_tree_workspace_bytes(cfg: rq_config, batch: int, n_nodes: int) -> int:
@@ -264,12 +278,12 @@ def rq_tree_attention(handle, layer, group, loop, batch, n_nodes, q, k_new, v_ne
     k_new, v_new: [batch, H, n_nodes, d] bf16; mask: [batch, n_nodes,
     ceil(n_nodes / 64)] int64 or uint64 bits, or None (a single sequence);
     node_counts: [batch] int32 or None."""
-    fn = "rq_tree_attention"
+    fn, dev = "rq_tree_attention", _device()
     _check(fn, lib.rq_tree_attention(
-        handle, layer, group, loop, batch, n_nodes, _arg(fn, q, _BF16), _arg(fn, k_new, _BF16),
-        _arg(fn, v_new, _BF16), _arg(fn, mask, _U64, batch * n_nodes * -(-n_nodes // 64)),
-        _arg(fn, node_counts, _I32, batch), _arg(fn, seq_lens, _I32, batch), softmax_scale, _arg(fn, out, _BF16),
-        _arg(fn, workspace, _U8, workspace_bytes), workspace_bytes, _stream(stream)))
+        handle, layer, group, loop, batch, n_nodes, _arg(fn, dev, q, "bf16"), _arg(fn, dev, k_new, "bf16"),
+        _arg(fn, dev, v_new, "bf16"), _arg(fn, dev, mask, "u64", batch * n_nodes * -(-n_nodes // 64)),
+        _arg(fn, dev, node_counts, "i32", batch), _arg(fn, dev, seq_lens, "i32", batch), softmax_scale, _arg(fn, dev, out, "bf16"),
+        _arg(fn, dev, workspace, "u8", workspace_bytes), workspace_bytes, _stream(stream)))
 
 
 def rq_pages_workspace_bytes(cfg: rq_config, num_pages: int) -> int:
@@ -278,40 +292,40 @@ def rq_pages_workspace_bytes(cfg: rq_config, num_pages: int) -> int:
 
 def rq_pages_copy(handle, n, src, dst, status=None, stream=None):
     """Copy page src[i] to page dst[i] of a paged cache, every layer and group."""
-    fn = "rq_pages_copy"
-    _check(fn, lib.rq_pages_copy(handle, n, _arg(fn, src, _I32, n), _arg(fn, dst, _I32, n),
-                                     _arg(fn, status, _I32, 4), _stream(stream)))
+    fn, dev = "rq_pages_copy", _device()
+    _check(fn, lib.rq_pages_copy(handle, n, _arg(fn, dev, src, "i32", n), _arg(fn, dev, dst, "i32", n),
+                                     _arg(fn, dev, status, "i32", 4), _stream(stream)))
 
 
 def rq_pages_fork(handle, n, src_rows, dst_rows, refs, status=None, stream=None):
     """Row dst_rows[i] shares the pages of row src_rows[i] and gives up its own."""
-    fn = "rq_pages_fork"
-    _check(fn, lib.rq_pages_fork(handle, n, _arg(fn, src_rows, _I32, n), _arg(fn, dst_rows, _I32, n),
-                                     _arg(fn, refs, _I32), _arg(fn, status, _I32, 4), _stream(stream)))
+    fn, dev = "rq_pages_fork", _device()
+    _check(fn, lib.rq_pages_fork(handle, n, _arg(fn, dev, src_rows, "i32", n), _arg(fn, dev, dst_rows, "i32", n),
+                                     _arg(fn, dev, refs, "i32"), _arg(fn, dev, status, "i32", 4), _stream(stream)))
 
 
 def rq_pages_reserve(handle, batch, seq_lens, n_tokens, refs, status, workspace, workspace_bytes, stream=None):
     """Give rows 0 .. batch-1 pages of their own for their next n_tokens positions
     (copy on write where a page is shared)."""
-    fn = "rq_pages_reserve"
-    _check(fn, lib.rq_pages_reserve(handle, batch, _arg(fn, seq_lens, _I32, batch), n_tokens, _arg(fn, refs, _I32),
-                                        _arg(fn, status, _I32, 4), _arg(fn, workspace, _U8, workspace_bytes),
+    fn, dev = "rq_pages_reserve", _device()
+    _check(fn, lib.rq_pages_reserve(handle, batch, _arg(fn, dev, seq_lens, "i32", batch), n_tokens, _arg(fn, dev, refs, "i32"),
+                                        _arg(fn, dev, status, "i32", 4), _arg(fn, dev, workspace, "u8", workspace_bytes),
                                         workspace_bytes, _stream(stream)))
 
 
 def rq_pages_free(handle, n, rows, keep, refs, status=None, stream=None):
     """Give up the pages of rows[i] behind its first keep[i] tokens (keep None: all)."""
-    fn = "rq_pages_free"
-    _check(fn, lib.rq_pages_free(handle, n, _arg(fn, rows, _I32, n), _arg(fn, keep, _I32, n), _arg(fn, refs, _I32),
-                                     _arg(fn, status, _I32, 4), _stream(stream)))
+    fn, dev = "rq_pages_free", _device()
+    _check(fn, lib.rq_pages_free(handle, n, _arg(fn, dev, rows, "i32", n), _arg(fn, dev, keep, "i32", n), _arg(fn, dev, refs, "i32"),
+                                     _arg(fn, dev, status, "i32", 4), _stream(stream)))
 
 
 def rq_pages_compact(handle, refs, used, status, workspace, workspace_bytes, stream=None):
     """Move the used pages to the front of the pool; used (int32 on the device)
     receives their number."""
-    fn = "rq_pages_compact"
-    _check(fn, lib.rq_pages_compact(handle, _arg(fn, refs, _I32), _arg(fn, used, _I32, 1), _arg(fn, status, _I32, 4),
-                                        _arg(fn, workspace, _U8, workspace_bytes), workspace_bytes,
+    fn, dev = "rq_pages_compact", _device()
+    _check(fn, lib.rq_pages_compact(handle, _arg(fn, dev, refs, "i32"), _arg(fn, dev, used, "i32", 1), _arg(fn, dev, status, "i32", 4),
+                                        _arg(fn, dev, workspace, "u8", workspace_bytes), workspace_bytes,
                                         _stream(stream)))
 
 
@@ -319,28 +333,29 @@ def rq_rope(cfg: rq_rope_config, q, k, start, offsets=None, q_out=None, k_out=No
     """Rotate q and k ([batch, heads, n, d] tensors of any strides with contiguous
     channels; either may be None) by positions start[b] + offsets[b, t] (offsets
     None: + t).  q_out, k_out None: in place."""
-    import torch
-    fn = "rq_rope"
-    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    fn, dev = "rq_rope", _device()
     first = q if q is not None else k
-    if first is None or first.dim() != 4 or first.dtype not in code:
+    if first is None or first.dim() != 4 or first.dtype not in _ROPE_DT:
         raise RqError(fn, 1)
-    batch, n = first.shape[0], first.shape[2]
+    dtype = first.dtype
+    batch, _, n, _ = first.shape
 
     def pack(x, y):
         if x is None:
             return None
-        y = x if y is None else y
-        for t in (x, y):
-            if (t.dim() != 4 or t.shape != x.shape or t.shape[0] != batch or t.shape[2] != n or t.dtype != first.dtype
-                    or t.shape[3] != cfg.head_dim or t.stride(3) != 1 or not t.is_cuda
-                    or t.device.index != torch.cuda.current_device()):
+        shape, xs = x.shape, x.stride()
+        if (len(shape) != 4 or x.dtype is not dtype or shape[0] != batch or shape[2] != n or shape[3] != cfg.head_dim
+                or xs[3] != 1 or x.get_device() != dev):
+            raise RqError(fn, 1)
+        if y is None or y is x:
+            y, ys = x, xs
+        else:
+            ys = y.stride()
+            if y.dtype is not dtype or y.shape != shape or ys[3] != 1 or y.get_device() != dev:
                 raise RqError(fn, 1)
-        return _rope_tensor(x.data_ptr(), y.data_ptr(), x.shape[1], x.stride(0), x.stride(1), x.stride(2),
-                            y.stride(0), y.stride(1), y.stride(2))
+        return _rope_tensor(x.data_ptr(), y.data_ptr(), shape[1], xs[0], xs[1], xs[2], ys[0], ys[1], ys[2])
 
     tq, tk = pack(q, q_out), pack(k, k_out)
-    _check(fn, lib.rq_rope(ctypes.byref(cfg), code[first.dtype], batch, n,
-                           ctypes.byref(tq) if tq is not None else None,
-                           ctypes.byref(tk) if tk is not None else None, _arg(fn, start, _I32, batch),
-                           _arg(fn, offsets, _I32, batch * n), _stream(stream)))
+    _check(fn, lib.rq_rope(ctypes.byref(cfg), _ROPE_DT[dtype], batch, n, None if tq is None else ctypes.byref(tq),
+                           None if tk is None else ctypes.byref(tk), _arg(fn, dev, start, "i32", batch),
+                           _arg(fn, dev, offsets, "i32", batch * n), _stream(stream)))

@@ -30,6 +30,7 @@
 // tensor memory then.  Sums stay in the lanes' registers until the unit ends.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include <cuda_fp8.h>
@@ -1452,8 +1453,16 @@ cudaError_t launch_tree_t(const TreeArgs& args, int num_sms, cudaStream_t stream
   TreeArgs a = args;
   a.pstride = C::PSTRIDE;
   auto* kern = tree_mma_kernel<D, GS, NRES, NB>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<int> ready[kMaxDevices];   // shared-memory limit set on this device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    ready[dev].store(1, std::memory_order_release);
+  }
   const int units = a.batch * a.g.H * a.nqb;
   e = launch_dependent(tree_prep_kernel<D, NRES, NB>, dim3(units * (NB / 16)), dim3(256), 0, stream, a);
   if (e != cudaSuccess) return e;
