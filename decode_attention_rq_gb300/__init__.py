@@ -258,8 +258,8 @@ def _device():
 def _arg(fn, dev, x, kind, count=0):
     """Address of x for a C call.  None and ints (device addresses) pass as they
     are; a tensor has to be contiguous, of the kind's dtype, on device dev (the one
-    current on this thread) and at least `count` long: a host pointer or a short
-    buffer would fault the device."""
+    current on this thread) and at least `count` long (0: the call's arguments do not
+    tell the length): a host pointer or a short buffer would fault the device."""
     if x is None or isinstance(x, int):
         return x
     if x.dtype not in _DT[kind] or x.get_device() != dev or x.numel() < count or not x.is_contiguous():
@@ -282,8 +282,9 @@ def rq_tree_attention(handle, layer, group, loop, batch, n_nodes, q, k_new, v_ne
     _check(fn, lib.rq_tree_attention(
         handle, layer, group, loop, batch, n_nodes, _arg(fn, dev, q, "bf16"), _arg(fn, dev, k_new, "bf16"),
         _arg(fn, dev, v_new, "bf16"), _arg(fn, dev, mask, "u64", batch * n_nodes * -(-n_nodes // 64)),
-        _arg(fn, dev, node_counts, "i32", batch), _arg(fn, dev, seq_lens, "i32", batch), softmax_scale, _arg(fn, dev, out, "bf16"),
-        _arg(fn, dev, workspace, "u8", workspace_bytes), workspace_bytes, _stream(stream)))
+        _arg(fn, dev, node_counts, "i32", batch), _arg(fn, dev, seq_lens, "i32", batch), softmax_scale,
+        _arg(fn, dev, out, "bf16"), _arg(fn, dev, workspace, "u8", workspace_bytes), workspace_bytes,
+        _stream(stream)))
 
 
 def rq_pages_workspace_bytes(cfg: rq_config, num_pages: int) -> int:
@@ -293,40 +294,44 @@ def rq_pages_workspace_bytes(cfg: rq_config, num_pages: int) -> int:
 def rq_pages_copy(handle, n, src, dst, status=None, stream=None):
     """Copy page src[i] to page dst[i] of a paged cache, every layer and group."""
     fn, dev = "rq_pages_copy", _device()
-    _check(fn, lib.rq_pages_copy(handle, n, _arg(fn, dev, src, "i32", n), _arg(fn, dev, dst, "i32", n),
-                                     _arg(fn, dev, status, "i32", 4), _stream(stream)))
+    _check(fn, lib.rq_pages_copy(
+        handle, n, _arg(fn, dev, src, "i32", n), _arg(fn, dev, dst, "i32", n), _arg(fn, dev, status, "i32", 4),
+        _stream(stream)))
 
 
 def rq_pages_fork(handle, n, src_rows, dst_rows, refs, status=None, stream=None):
     """Row dst_rows[i] shares the pages of row src_rows[i] and gives up its own."""
     fn, dev = "rq_pages_fork", _device()
-    _check(fn, lib.rq_pages_fork(handle, n, _arg(fn, dev, src_rows, "i32", n), _arg(fn, dev, dst_rows, "i32", n),
-                                     _arg(fn, dev, refs, "i32"), _arg(fn, dev, status, "i32", 4), _stream(stream)))
+    _check(fn, lib.rq_pages_fork(
+        handle, n, _arg(fn, dev, src_rows, "i32", n), _arg(fn, dev, dst_rows, "i32", n), _arg(fn, dev, refs, "i32"),
+        _arg(fn, dev, status, "i32", 4), _stream(stream)))
 
 
 def rq_pages_reserve(handle, batch, seq_lens, n_tokens, refs, status, workspace, workspace_bytes, stream=None):
     """Give rows 0 .. batch-1 pages of their own for their next n_tokens positions
     (copy on write where a page is shared)."""
     fn, dev = "rq_pages_reserve", _device()
-    _check(fn, lib.rq_pages_reserve(handle, batch, _arg(fn, dev, seq_lens, "i32", batch), n_tokens, _arg(fn, dev, refs, "i32"),
-                                        _arg(fn, dev, status, "i32", 4), _arg(fn, dev, workspace, "u8", workspace_bytes),
-                                        workspace_bytes, _stream(stream)))
+    _check(fn, lib.rq_pages_reserve(
+        handle, batch, _arg(fn, dev, seq_lens, "i32", batch), n_tokens, _arg(fn, dev, refs, "i32"),
+        _arg(fn, dev, status, "i32", 4), _arg(fn, dev, workspace, "u8", workspace_bytes), workspace_bytes,
+        _stream(stream)))
 
 
 def rq_pages_free(handle, n, rows, keep, refs, status=None, stream=None):
     """Give up the pages of rows[i] behind its first keep[i] tokens (keep None: all)."""
     fn, dev = "rq_pages_free", _device()
-    _check(fn, lib.rq_pages_free(handle, n, _arg(fn, dev, rows, "i32", n), _arg(fn, dev, keep, "i32", n), _arg(fn, dev, refs, "i32"),
-                                     _arg(fn, dev, status, "i32", 4), _stream(stream)))
+    _check(fn, lib.rq_pages_free(
+        handle, n, _arg(fn, dev, rows, "i32", n), _arg(fn, dev, keep, "i32", n), _arg(fn, dev, refs, "i32"),
+        _arg(fn, dev, status, "i32", 4), _stream(stream)))
 
 
 def rq_pages_compact(handle, refs, used, status, workspace, workspace_bytes, stream=None):
     """Move the used pages to the front of the pool; used (int32 on the device)
     receives their number."""
     fn, dev = "rq_pages_compact", _device()
-    _check(fn, lib.rq_pages_compact(handle, _arg(fn, dev, refs, "i32"), _arg(fn, dev, used, "i32", 1), _arg(fn, dev, status, "i32", 4),
-                                        _arg(fn, dev, workspace, "u8", workspace_bytes), workspace_bytes,
-                                        _stream(stream)))
+    _check(fn, lib.rq_pages_compact(
+        handle, _arg(fn, dev, refs, "i32"), _arg(fn, dev, used, "i32", 1), _arg(fn, dev, status, "i32", 4),
+        _arg(fn, dev, workspace, "u8", workspace_bytes), workspace_bytes, _stream(stream)))
 
 
 def rq_rope(cfg: rq_rope_config, q, k, start, offsets=None, q_out=None, k_out=None, stream=None):

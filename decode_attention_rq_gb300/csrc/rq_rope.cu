@@ -4,8 +4,10 @@
 //   (a', b') = m (a cos - b sin, b cos + a sin);
 // the inverse call negates the angle, which is the transposed map and so the
 // gradient.  The fraction of a turn of position p is p * F mod 1 with F = f / 2 pi
-// as a 64-bit binary fraction: one wrapping integer product, exact but for the
-// rounding of F, taken in float64 (2^-55 of a turn a position, 2^-24 at the farthest).
+// as a 64-bit binary fraction: one wrapping integer product, exact but for F itself,
+// which is taken in float64.  f_i is a product of i equal ratios, each off by at most
+// 2^-52 of itself with its rounding; i f_i <= r / (2 e ln theta), 5.2 at r = 256 and theta =
+// 10^4, so that F is off by less than 2^-51 (2^-20 of a turn at the farthest position).
 // sin and cos are then taken of a reduced float32 argument.
 //
 // Memory-bound: every element is read and written once.
@@ -271,7 +273,8 @@ extern "C" rq_status rq_rope(const rq_rope_config* cfg, int32_t dtype, int32_t b
   const int d = cfg->head_dim, r = cfg->rotary_dim;
   if (d < 2 || d > 512 || r < 2 || r > 2 * kMaxPairs || r > d || (r & 1)) return RQ_ERR_UNSUPPORTED;
   if (cfg->scaling < RQ_ROPE_PLAIN || cfg->scaling > RQ_ROPE_PARTS) return RQ_ERR_INVALID_ARG;
-  if (!(cfg->theta > 1.0) || !std::isfinite(cfg->theta) || !std::isfinite(cfg->magnitude)) return RQ_ERR_INVALID_ARG;
+  if (!(cfg->theta > 1.0) || !std::isfinite(cfg->theta) || !std::isfinite((float)cfg->magnitude))
+    return RQ_ERR_INVALID_ARG;
   if (cfg->scaling != RQ_ROPE_PLAIN && !(cfg->factor > 0.0 && std::isfinite(cfg->factor))) return RQ_ERR_INVALID_ARG;
   if (cfg->scaling == RQ_ROPE_BASE && r == 2) return RQ_ERR_INVALID_ARG;   // r / (r - 2)
   if (cfg->scaling == RQ_ROPE_PARTS && !(cfg->original_len > 0 && cfg->low_turns < cfg->high_turns &&
@@ -283,6 +286,9 @@ extern "C" rq_status rq_rope(const rq_rope_config* cfg, int32_t dtype, int32_t b
     if (!x) continue;
     if (x->heads <= 0 || ((!x->in || !x->out) && batch > 0 && n > 0)) return RQ_ERR_INVALID_ARG;   // empty: any pointer
     if (!aligned_to(x->in, es) || !aligned_to(x->out, es)) return RQ_ERR_ALIGNMENT;
+    // two results in one place
+    if ((batch > 1 && x->out_row == 0) || (x->heads > 1 && x->out_head == 0) || (n > 1 && x->out_token == 0))
+      return RQ_ERR_INVALID_ARG;
     heads += x->heads;
   }
   if (!aligned_to(start, 4) || !aligned_to(offsets, 4)) return RQ_ERR_ALIGNMENT;
@@ -310,6 +316,7 @@ extern "C" rq_status rq_rope(const rq_rope_config* cfg, int32_t dtype, int32_t b
       keep = keep < 0 ? 0 : (keep > 1 ? 1 : keep);
       s = f * (keep + (1 - keep) / cfg->factor);
     }
+    if (!std::isfinite(s)) return RQ_ERR_INVALID_ARG;   // a factor near zero
     double turns = s / kTwoPi;
     turns -= std::floor(turns);
     unsigned long long u = (unsigned long long)(turns * 0x1p63) << 1;   // turns < 1: below 2^63

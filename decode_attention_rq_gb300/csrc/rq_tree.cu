@@ -239,8 +239,11 @@ cudaError_t launch_tree(const rq_cache& c, int layer, int group, int loop, int b
   const bool chained = (c.geom.mode & RQ_MODE_CHAINED) != 0;
   a.nres = loop == c.geom.P - 1 ? 0 : (chained ? c.geom.P - 1 - loop : 1);
   a.qscale = scale * kLog2e;
+  if ((int64_t)batch * c.geom.Hq * n_nodes > (1 << 30)) return cudaErrorNotSupported;   // blocks are int32
   if (!chained) {
     const int nb = tree_nb(c.geom.qpk * n_nodes);
+    const int64_t units = (int64_t)batch * c.geom.H * ((c.geom.qpk * n_nodes + nb - 1) / nb);
+    if (units * ((c.geom.Nmax + kTreeStep - 1) / kTreeStep) > 0x7fffffff) return cudaErrorNotSupported;   // steps, too
     const TreeSpace w = tree_space(c.geom, batch, n_nodes, c.num_sms);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.M = c.geom.qpk * n_nodes;

@@ -361,15 +361,16 @@ size_t rq_tree_workspace_bytes(const rq_config* cfg, int32_t batch, int32_t n_no
  *   seq_lens     device int32 [batch]
  *   out          device bf16 [batch][Hq][T][d]; zero for a node that sees no key
  * A K or V that a node's mask hides does not enter that node's result, not even
- * when it is infinite or NaN.  q is scaled per node by a power of two and kept
- * in 16-bit floating point (11 significant bits), as are the rebuilt K/V and the
+ * when it is infinite or NaN.  q (finite: up to 2^120 in magnitude) is scaled per
+ * node by a power of two and kept in 16-bit floating point (11 significant bits), as are the rebuilt K/V and the
  * softmax weights (rebuilt K/V up to 65504); scores, softmax sums and
  * accumulators are float32.
  * With T = 1 and a mask that names the token itself this is
  * rq_decode_attention with a BF16 result.
  * Chained caches (RQ_MODE_CHAINED) are read as rq_decode_attention reads them.
  * Errors: as rq_decode_attention; INVALID_ARG (n_nodes < 1), UNSUPPORTED
- * (n_nodes > RQ_MAX_TREE_NODES, batch > RQ_MAX_DECODE_BATCH). */
+ * (n_nodes > RQ_MAX_TREE_NODES, batch > RQ_MAX_DECODE_BATCH, more than 2^30
+ * queries, batch * H * ceil(Hq / H * T / 64) * ceil(max_seq_len / 128) > 2^31 - 1). */
 rq_status rq_tree_attention(rq_cache* cache, int32_t layer, int32_t group, int32_t loop,
                             int32_t batch, int32_t n_nodes, const void* q, const void* k_new,
                             const void* v_new, const uint64_t* mask, const int32_t* node_counts,
@@ -480,8 +481,9 @@ typedef struct rq_rope_config {
 
 /* One tensor [batch][heads][n][d] read and written by rq_rope: the element
  * strides of row, head and token; channels are contiguous.  Any strides do;
- * pointers and strides that are multiples of 16 bytes are faster.  out may be
- * in (with the same strides); otherwise the two must not overlap. */
+ * pointers and strides that are multiples of 16 bytes are faster.  out's elements
+ * are distinct (a stride of zero over several rows, heads or tokens is refused).
+ * out may be in (with the same strides); otherwise the two must not overlap. */
 typedef struct rq_rope_tensor {
   const void* in;
   void* out;
@@ -495,15 +497,16 @@ typedef struct rq_rope_tensor {
  * are start[b] + offsets[b][t], offsets NULL: start[b] + t, so with start =
  * seq_lens a prompt, a decoded token (n = 1) or the nodes of a drafted tree
  * (offsets = their depths) sit where they belong.  Angles are taken modulo a
- * turn in 64-bit fixed point (off by 2^-55 of a turn a position, 2^-24 at the
- * farthest).  Arithmetic is float32, rounded once to the tensors' type.
+ * turn in 64-bit fixed point from float64 frequencies: off by less than 2^-51 of
+ * a turn a position for theta >= 10000, 2^-20 at the farthest.  Arithmetic is
+ * float32, rounded once to the tensors' type.
  *   dtype    rq_dtype of every tensor
  *   q, k     host; k (or q) may be NULL
  *   start    device int32 [batch], or NULL: zeros
  *   offsets  device int32 [batch][n] or NULL
  * The tensors need only be aligned to their element.
- * Errors: INVALID_ARG (null, bad count or config), ALIGNMENT, UNSUPPORTED
- * (head_dim or rotary_dim outside the ranges, heads x batch > 2^30), CUDA. */
+ * Errors: INVALID_ARG (null, bad count or config, frequencies that are not
+ * finite, out strides of zero), ALIGNMENT, UNSUPPORTED (head_dim or rotary_dim outside the ranges, heads x batch > 2^30), CUDA. */
 rq_status rq_rope(const rq_rope_config* cfg, int32_t dtype, int32_t batch, int32_t n,
                   const rq_rope_tensor* q, const rq_rope_tensor* k, const int32_t* start,
                   const int32_t* offsets, void* stream);

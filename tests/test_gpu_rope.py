@@ -2,8 +2,8 @@
 
 Bars.  A result is one rounding to the tensors' type (half a step: 2^-8 BF16,
 2^-11 FP16, 2^-24 FP32 of the value) of a float32 sum a cos -+ b sin: two products and
-one sum (3 * 2^-24 of |a| + |b|), and cos, sin to within 2^-22 (float32 sincospi of an
-argument rounded to 2^-24 of half a turn: pi * 2^-25, plus two units of the function).
+one sum (3 * 2^-24 of |a| + |b|), and cos, sin to within 2^-22 (float32 series of an
+argument of at most pi / 4, rounded twice: 2 * 2^-24 * pi / 4, plus two units of the series).
 |gpu - float64| <= step * |x| + magnitude * (|a| + |b|) * 2^-21.  FP16 values below the
 normal range add half their step, 2^-25.
 """
