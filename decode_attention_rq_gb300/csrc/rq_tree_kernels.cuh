@@ -334,12 +334,17 @@ struct TreeCfg {
   static constexpr int IMG = PL * (D / 16) * QSTEP;        // query operand of a unit
   static constexpr int PBUF = kTreeStep * 128;             // weights: 128-byte row per token
   static constexpr int TAB = PL * NG * 64 * 8 + NRES * 256; // V constants
-  static constexpr int FIX = 2 * IMG + PBUF + TAB;
+  // tables of V constants: two (one barrier a step less) where they leave room for four stages
+  static constexpr int TABS = 2 * IMG + PBUF + 2 * TAB + 4 * STAGE + 6144 <= 226 * 1024 ? 2 : 1;
+  static constexpr int FIX = 2 * IMG + PBUF + TABS * TAB;
   static constexpr int STAGES = FIX + 4 * STAGE + 6144 <= 226 * 1024 ? 4 : 3;
   static constexpr int SMEM = FIX + STAGES * STAGE + 1024;
   // tensor memory columns
   static constexpr int KA = 0, KR = 64, VA = 128, VR = 192, OA = 256, OR = 256 + NB, S0 = 256 + 2 * NB;
-  static constexpr int SCOLS = 2 * NB;                     // Sa, Sr
+  // scores: two buffers where they fit and the softmax is the longer for its coefficients (32 queries:
+  // 57.6 -> 56.2 us at 8k, batch 4; the anchor loop is not faster with two)
+  static constexpr int SBUF = NRES && NB <= 32 ? 2 : 1;
+  static constexpr int SCOLS = SBUF * PL * NB;             // Sa, Sr
   static_assert(S0 + SCOLS <= 512, "tensor memory");
   static_assert(SMEM <= 227 * 1024 - 5120, "shared memory");
   static constexpr int NS = NB / 32 > 1 ? 2 : 1, NQ = NB / NS;   // softmax groups, queries of each
@@ -481,6 +486,34 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
   }
 }
 
+// Every query's maximum or sum over the warp's lanes, to row: a reduce-scatter, each step halving
+// what a lane holds (31 exchanges for 32 queries, against 160)
+template <int NQ, bool MAX>
+__device__ __forceinline__ void tree_spread(float (&x)[NQ], float* row, int lane) {
+#pragma unroll
+  for (int o = 16, n = NQ / 2; o >= 1; o >>= 1) {
+    if (n >= 1) {
+      const bool up = (lane & o) != 0;
+#pragma unroll
+      for (int i = 0; i < NQ / 2; ++i)
+        if (i < n) {
+          const float send = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
+          const float y = __shfl_xor_sync(0xffffffffu, send, o);
+          x[i] = MAX ? fmaxf(keep, y) : keep + y;
+        }
+      n >>= 1;
+    } else {
+      const float y = __shfl_xor_sync(0xffffffffu, x[0], o);
+      x[0] = MAX ? fmaxf(x[0], y) : x[0] + y;
+    }
+  }
+  // 32 queries: one a lane; 16: one for two lanes
+  if (NQ == 32)
+    row[lane] = x[0];
+  else if ((lane & 1) == 0)
+    row[lane >> 1] = x[0];
+}
+
 // ---- the streaming kernel --------------------------------------------------------
 template <int D, int GS, int NRES, int NB>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
@@ -488,7 +521,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
   constexpr int ST = C::STAGES, NG = C::NG, PL = C::PL;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full_bar[ST], empty_bar[ST], qfull_bar[2], qempty_bar[2], kfull_bar[2], kempty_bar[2],
-      vfull_bar[2], vempty_bar[2], sfull_bar, sempty_bar, pfull_bar, pempty_bar, drain_bar[2];
+      vfull_bar[2], vempty_bar[2], sfull_bar[2], sempty_bar[2], pfull_bar, pempty_bar, drain_bar[2];
   __shared__ TreeRowsShared rows_s;
   __shared__ __align__(16) float qm_s[NB / 2][4];   // two queries: their scales, minus their references
   __shared__ __align__(16) float f_s[NB];
@@ -502,7 +535,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
   uint8_t* q_img = smem;                                  // two query operands
   uint8_t* p_buf = q_img + 2 * C::IMG;                    // weights
   uint8_t* stages = p_buf + C::PBUF;
-  uint8_t* tab = stages + ST * C::STAGE;
+  uint8_t* tabs = stages + ST * C::STAGE;                 // V constants
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int per = a.g.H * a.nqb;
@@ -514,8 +547,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       mbar_init(&qfull_bar[i], 1); mbar_init(&qempty_bar[i], 1);
       mbar_init(&kfull_bar[i], 4); mbar_init(&kempty_bar[i], 1);
       mbar_init(&vfull_bar[i], i ? 4 : 4 * C::NVA); mbar_init(&vempty_bar[i], 1);
+      mbar_init(&sfull_bar[i], 1); mbar_init(&sempty_bar[i], 4 * C::NS);
     }
-    mbar_init(&sfull_bar, 1); mbar_init(&sempty_bar, 4 * C::NS);
     mbar_init(&pfull_bar, 4 * C::NS); mbar_init(&pempty_bar, 1);
     mbar_init(&drain_bar[0], 1); mbar_init(&drain_bar[1], 1);
     fence_mbar_init();
@@ -549,6 +582,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     a.status[0] = 1;
     return false;
   };
+  // buffer and phase of step `it`'s scores
+  auto s_buf = [](int it) { return C::SBUF == 2 ? it & 1 : 0; };
+  auto s_par = [](int it) { return (uint32_t)(C::SBUF == 2 ? it >> 1 : it) & 1; };
   // the same by a whole warp, which goes on together (the tcgen05 loads and stores are warp-wide)
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
     (void)wait(bar, parity);
@@ -575,7 +611,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       wait_warp(&full_bar[st], par);
       const uint8_t* s = stages + st * C::STAGE;
       const bool on = lt < (info_s[it & 7].x & 255);
-      v_sync();   // the previous step's constants are used up
+      // the step's table: the one before is still in use; with a single one, wait until it is not
+      uint8_t* tab = tabs + (C::TABS == 2 ? (it & 1) * C::TAB : 0);
+      if (C::TABS == 1) v_sync();
       // Constants of this lane's token.  The anchor's coefficient c = m f, f a power of two and
       // 1 <= |m| < 2: f goes into the constants, where powers of two are exact, and m multiplies the
       // finished f (s code + o), so that a value is rounded relative to itself and not to its group's
@@ -762,19 +800,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         ++seg;
         wait(&qfull_bar[seg & 1], (seg >> 1) & 1);
       }
-      wait(&sempty_bar, (it & 1) ^ 1);
+      wait(&sempty_bar[s_buf(it)], s_par(it) ^ 1);
 #pragma unroll
       for (int pl = 0; pl < PL; ++pl) {
         if (pl) wait(&kfull_bar[pl], it & 1);
         tc_after();
         __syncwarp();
         if (elect_one()) {
-          tc_chain<D / 16>(tmem + C::S0 + pl * NB, tmem + (pl ? C::KR : C::KA),
+          tc_chain<D / 16>(tmem + C::S0 + (s_buf(it) * PL + pl) * NB, tmem + (pl ? C::KR : C::KA),
                            q_lo + (((seg & 1) * C::IMG + pl * (D / 16) * C::QSTEP) >> 4), kDescHiQ, C::QSTEP >> 4,
                            tc_idesc(NB, false), true);
           tc_commit(&kempty_bar[pl]);
           if (pl == PL - 1) {
-            tc_commit(&sfull_bar);
+            tc_commit(&sfull_bar[s_buf(it)]);
             if (flags & 512) tc_commit(&qempty_bar[seg & 1]);
           }
         }
@@ -827,7 +865,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
     uint32_t par = 0;
 #pragma unroll 1
     for (int it = 0; it < n_it; ++it) {
-      if (NRES) wait_warp(&full_bar[st], par); else wait_warp(&sfull_bar, it & 1);
+      if (NRES) wait_warp(&full_bar[st], par); else wait_warp(&sfull_bar[s_buf(it)], s_par(it));
       const int2 info = info_s[it & 7];
       const bool first = (info.x & 256) != 0, on = lt < (info.x & 255);
       const int unit = info.y;
@@ -848,11 +886,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty_bar[st]);
         if (++st == ST) { st = 0; par ^= 1; }
-        wait_warp(&sfull_bar, it & 1);
+        wait_warp(&sfull_bar[s_buf(it)], s_par(it));
       }
       const float2 c2 = make_float2(c, c);
       tc_after();
-      const uint32_t s0 = lanes + C::S0 + q_at;
+      const uint32_t s0 = lanes + C::S0 + s_buf(it) * PL * NB + q_at;
       // score products of 16 queries with this lane's token
       auto scores = [&](int ch, float2 (&y)[8]) {
         uint32_t ra[16], rr[16];
@@ -889,18 +927,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       }
       if (__builtin_expect(wg_any(my_bar, on && top > kTop), 0)) {
         // move the references to this step's maxima where those are higher
+        float top_q[NQ];
 #pragma unroll
         for (int ch = 0; ch < NQ / 16; ++ch) {
           float2 y[8];
           scores(ch, y);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float v = on ? (i & 1 ? y[i / 2].y : y[i / 2].x) * qm[8 * ch + i / 2][i & 1] : -INFINITY;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-            if (lane == 0) wred_s[w4][q_at + 16 * ch + i] = v;
-          }
+          for (int i = 0; i < 16; ++i)
+            top_q[16 * ch + i] = on ? (i & 1 ? y[i / 2].y : y[i / 2].x) * qm[8 * ch + i / 2][i & 1] : -INFINITY;
         }
+        tree_spread<NQ, true>(top_q, wred_s[w4] + q_at, lane);
         wg_sync(my_bar);
         if (lt < NQ) {
           const float old = -qm[lt >> 1][2 + (lt & 1)];
@@ -942,7 +978,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       // the scores are in registers: their place in tensor memory is free
       tc_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sempty_bar);
+      if (lane == 0) mbar_arrive(&sempty_bar[s_buf(it)]);
       wait_warp(&pempty_bar, (it & 1) ^ 1);
       uint8_t* prow = p_buf + slot * 128;
 #pragma unroll
@@ -987,27 +1023,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
           }
         }
         tc_before();
-        // sums over the lanes: reduce-scatter, then over the warps in order
-#pragma unroll
-        for (int o = 16, n = NQ / 2; o >= 1; o >>= 1) {
-          if (n >= 1) {
-            const bool up = (lane & o) != 0;
-#pragma unroll
-            for (int i = 0; i < NQ / 2; ++i)
-              if (i < n) {
-                const float send = up ? l[i] : l[i + n], keep = up ? l[i + n] : l[i];
-                l[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-              }
-            n >>= 1;
-          } else {
-            l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
-          }
-        }
-        // 32 queries: one a lane; 16: one for two lanes
-        if (NQ == 32)
-          wred_s[w4][q_at + lane] = l[0];
-        else if ((lane & 1) == 0)
-          wred_s[w4][lane >> 1] = l[0];
+        tree_spread<NQ, false>(l, wred_s[w4] + q_at, lane);   // then over the warps in order
         wg_sync(my_bar);
         if (lt < NQ) {
           const int q = q_at + lt;
