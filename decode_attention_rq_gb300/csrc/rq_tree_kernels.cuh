@@ -1182,8 +1182,11 @@ constexpr int kDraftPitch = 272;       // bytes of a staged row: rows 4 banks ap
 constexpr int kMergeChunk = 32;        // partial states whose weights are held at a time
 
 template <int D, int NRES, int NB, int MQ>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, int ctas) {
+__global__ void __launch_bounds__(kMergeThreads, NRES && MQ == 8 ? 2 : 4) tree_merge_kernel(TreeArgs a, int ctas) {
   constexpr int NT = MQ / 8, PARTS = kMergeThreads / MQ;
+  // R^T loaded ahead in 64 registers, or, where many CTAs share an SM, when it is needed (4 CTAs an SM, not
+  // 2: grouped-query batch 8 129 -> 124 us; 128 CTAs of 8 queries are 3 us slower that way)
+  constexpr bool AHEAD = NRES && MQ == 8;
   __shared__ TreeRowsShared rows_s;
   __shared__ __align__(16) uint8_t kv_s[128 * kDraftPitch];   // drafted keys, then values
   __shared__ __align__(16) __nv_bfloat16 q_s[MQ][D + 8];
@@ -1228,16 +1231,18 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, i
   for (int i = tid; i < MQ * RC; i += kMergeThreads)
     *reinterpret_cast<uint4*>(&q_s[i / RC][(i % RC) * 8]) = i / RC < nq ? __ldg(qp + i) : make_uint4(0u, 0u, 0u, 0u);
   if (cnt > 0) stage(kp, 0);
-  // R^T, rows (output channels) 16 warp + g, + 8, as two pieces
-  uint32_t rhi[NRES ? D / 16 : 1][4], rlo[NRES ? D / 16 : 1][4];
-  if (dense) {
+  // R^T, rows (output channels) 16 warp + g, + 8, columns 16 k .., as two pieces
+  auto r_pieces = [&](int k, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k)
+    for (int i = 0; i < 4; ++i) {
+      const float* rp = a.R + (size_t)(16 * k + 2 * t4 + (i >> 1) * 8) * D + 16 * warp + g + (i & 1) * 8;
+      bf16_pieces(make_float2(__ldg(rp), __ldg(rp + D)), hi[i], lo[i]);
+    }
+  };
+  uint32_t rhi[AHEAD ? D / 16 : 1][4], rlo[AHEAD ? D / 16 : 1][4];
+  if (AHEAD && dense) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float* rp = a.R + (size_t)(16 * k + 2 * t4 + (i >> 1) * 8) * D + 16 * warp + g + (i & 1) * 8;
-        bf16_pieces(make_float2(__ldg(rp), __ldg(rp + D)), rhi[k][i], rlo[k][i]);
-      }
+    for (int k = 0; k < D / 16; ++k) r_pieces(k, rhi[AHEAD ? k : 0], rlo[AHEAD ? k : 0]);
   }
   for (int i = tid; i < MQ * (RQ_MAX_TREE_NODES / 64); i += kMergeThreads) {
     const int qi = i % MQ, w = i / MQ, t = (r0 + qi) % a.T;
@@ -1428,8 +1433,10 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, i
     float d[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k)
+#pragma unroll(AHEAD ? D / 16 : 2)
+    for (int k = 0; k < D / 16; ++k) {
+      if (!AHEAD) r_pieces(k, rhi[0], rlo[0]);
+      const uint32_t(&hi)[4] = rhi[AHEAD ? k : 0], (&lo)[4] = rlo[AHEAD ? k : 0];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         uint32_t bh2[2], bl2[2];
@@ -1438,10 +1445,11 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, i
           const int kk = 16 * k + 2 * t4 + 8 * i;
           bf16_pieces(make_float2(p_s[kk][8 * n + g], p_s[kk + 1][8 * n + g]), bh2[i], bl2[i]);
         }
-        mma_bf16(d[n], rhi[k], bh2[0], bh2[1]);
-        mma_bf16(d[n], rlo[k], bh2[0], bh2[1]);
-        mma_bf16(d[n], rhi[k], bl2[0], bl2[1]);
+        mma_bf16(d[n], hi, bh2[0], bh2[1]);
+        mma_bf16(d[n], lo, bh2[0], bh2[1]);
+        mma_bf16(d[n], hi, bl2[0], bl2[1]);
       }
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float* h = h_s + (8 * n + 2 * t4) * HP + 16 * warp + g;

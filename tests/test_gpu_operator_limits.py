@@ -50,6 +50,24 @@ def test_many_query_heads_of_a_key_head(d, Hq, H, T, chained):
     gpu.close()
 
 
+@pytest.mark.parametrize("d,rotation,loops", [(128, "dense", (0, 3)), (128, "hadamard", (1,)), (96, "dense", (2, 3))])
+def test_enough_queries_for_blocks_of_16_in_the_merge(d, rotation, loops):
+    """160 (row, KV head) pairs of 17 queries: 320 merge blocks of 16, more than two an SM."""
+    B, H, T, n = 10, 16, 17, 70
+    case = Case(L=1, P=4, G=1, H=H, d=d, g=32, B=B, Nmax=n, rotation=rotation)
+    gpu, obuf, geom, R = filled(case, 77, n)
+    rng = np.random.default_rng(14)
+    lens, counts = [n - 7 * b for b in range(B)], [T - (b % 4) for b in range(B)]
+    see, scale = tree_masks(15, B, T), 1 / math.sqrt(d)
+    for loop in loops:
+        qb, q = bf16(rng, B, H, T, d)
+        kb, kn = bf16(rng, B, H, T, d)
+        vb, vn = bf16(rng, B, H, T, d)
+        out = call(gpu, 0, 0, loop, qb, kb, vb, mask_words(see), counts, lens, scale)
+        check(out, reference(obuf, geom, R, case, 0, 0, loop, q, kn, vn, see, counts, lens, scale), f"loop {loop}")
+    gpu.close()
+
+
 def test_more_rows_than_a_warp():
     """70 rows, some of them empty: the work's split over rows is summed 32 at a time."""
     B, T = 70, 3
