@@ -28,6 +28,13 @@
 // reference of a query therefore moves only when some score exceeds it by 2^8 (the first
 // step, then rarely): weights stay below 2^14, in f16 range, and O is rescaled in
 // tensor memory then.  Sums stay in the lanes' registers until the unit ends.
+//
+// Measured (GB300; the three launches of a call, inputs cold): 16 heads of 128, residual loop, 8192 tokens,
+// 4 rows of 16 nodes 54 us, of which the streaming kernel 44 (120 MB: 2.7 TB/s in it, 2.2 TB/s over the call); 16384
+// tokens paged, 2 rows of 61 nodes 73 us; 8 rows of 13 nodes, 4 query heads a KV head 121 us; anchor loop, 55 heads
+// of 96, 4096 tokens, 2 rows of 25 nodes 36 us.  Not bound by memory: dequantizing 256 channels x 128 tokens of K and
+// V a step, with the softmax, keeps the schedulers at 0.66 instructions a clock (0.60 with 64 queries)
+// and each role's chain of waits at about 2600 clocks a step; the tensor pipe is 9 to 25 % busy.
 #pragma once
 
 #include <atomic>
@@ -121,9 +128,11 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
+// N products, one behind the other.  A loop: unrolled it saves 30 clocks a product and costs instruction cache
+// (54.7 -> 54.2 us at 8k, 36.4 -> 37.3 in the anchor loop).
 template <int N>
-__device__ __forceinline__ void tc_chain(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t b_step, uint32_t idesc,
-                                         bool fresh) {
+__device__ __forceinline__ void tc_chain(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t b_step,
+                                         uint32_t idesc, bool fresh) {
   const uint64_t b0 = (uint64_t)b_hi << 32 | b_lo;
   if (fresh) tc_mma<false>(d, a, b0, idesc); else tc_mma<true>(d, a, b0, idesc);
 #pragma unroll 1
@@ -171,6 +180,7 @@ constexpr uint32_t kDescHiQ = (256u >> 4) | 1u << 14 | 6u << 29, kDescHiP = (102
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr & 0x3FFFF) >> 4 | (1024u >> 4) << 16; }
 // Named barrier of one warpgroup; wg_any: true when any thread's predicate holds.
 __device__ __forceinline__ void wg_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+// the same of two warpgroups
 __device__ __forceinline__ void wg_sync2(int id) { asm volatile("barrier.cta.sync %0, 256;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool wg_any(int id, bool p) {
   uint32_t r;
@@ -182,8 +192,10 @@ __device__ __forceinline__ bool wg_any(int id, bool p) {
       : "memory");
   return r != 0;
 }
-template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -341,8 +353,8 @@ struct TreeCfg {
   static constexpr int SMEM = FIX + STAGES * STAGE + 1024;
   // tensor memory columns
   static constexpr int KA = 0, KR = 64, VA = 128, VR = 192, OA = 256, OR = 256 + NB, S0 = 256 + 2 * NB;
-  // scores: two buffers where they fit and the softmax is the longer for its coefficients (32 queries:
-  // 57.6 -> 56.2 us at 8k, batch 4; the anchor loop is not faster with two)
+  // scores: two buffers where they fit and the softmax is the longer for its coefficients (57.6 ->
+  // 56.2 us at 8k, batch 4, 16 queries; the anchor loop is not faster with two)
   static constexpr int SBUF = NRES && NB <= 32 ? 2 : 1;
   static constexpr int SCOLS = SBUF * PL * NB;             // Sa, Sr
   static_assert(S0 + SCOLS <= 512, "tensor memory");
@@ -359,11 +371,13 @@ struct TreeCfg {
 };
 
 // ---- query prep --------------------------------------------------------------------
-// One CTA per 16 queries of a unit: x and R x as f16 times a power of two of the query's own (its largest
+// One CTA per QP queries of a unit: x and R x as f16 times a power of two of the query's own (its largest
 // component to 2^10 .. 2^11: R keeps norms, so both stay below 2^15), in the layout of the B
 // operand.  x is BF16 and so exact; R x is a product on the 16-bit tensor cores with R as two
 // BF16 pieces (16 bits, against the 11 of its result), summed in float32: 8 warps with 16 rows
 // of R each in registers, one pass over the queries.
+// Bound by latency: R, the queries and the barriers in turn, 9 us cold at 64 units of 16 queries (6 in the
+// anchor loop); the loads of R come ahead of the wait for the kernel before.
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -378,18 +392,18 @@ __device__ __forceinline__ void bf16_pieces(float2 x, uint32_t& hi, uint32_t& lo
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-template <int D, int NRES, int NB>
+template <int D, int NRES, int NB, int QP>
 __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
   constexpr int PL = 1 + NRES;
   constexpr int IMG = PL * (D / 16) * NB * 32;
   constexpr int PITCH = D + 8;             // BF16 elements: rows 4 banks apart
   constexpr int RPITCH = D + 4;
-  constexpr int QP = 16;                   // queries of this CTA
   __shared__ __align__(16) __nv_bfloat16 q_s[QP][PITCH];
   __shared__ __align__(16) float r_s[NRES ? QP : 1][RPITCH];
   __shared__ float up_s[QP];               // the query's power of two
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  const int unit = blockIdx.x / (NB / QP), q0 = blockIdx.x % (NB / QP) * QP, qb = unit % a.nqb, bh = unit / a.nqb, b = bh / a.g.H;
+  const int unit = blockIdx.x / (NB / QP), q0 = blockIdx.x % (NB / QP) * QP;
+  const int qb = unit % a.nqb, bh = unit / a.nqb, b = bh / a.g.H;
   const bool hadamard = (a.g.mode & RQ_MODE_HADAMARD) != 0;
   uint32_t hi[NRES ? D / 16 : 1][4], lo[NRES ? D / 16 : 1][4];
   if (NRES && !hadamard && warp < D / 16) {   // R does not change while the cache is used: before the wait
@@ -398,7 +412,8 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(TreeArgs a) {
     for (int k = 0; k < D / 16; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i)   // rows g, g + 8; columns 2 t4, 2 t4 + 8
-        bf16_pieces(__ldg(reinterpret_cast<const float2*>(rp + (i & 1) * 8 * D + 16 * k + (i >> 1) * 8)), hi[k][i], lo[k][i]);
+        bf16_pieces(__ldg(reinterpret_cast<const float2*>(rp + (i & 1) * 8 * D + 16 * k + (i >> 1) * 8)), hi[k][i],
+                    lo[k][i]);
   }
   pdl_wait();
   pdl_launch_dependents();   // what ran before the call is complete: the next kernel may read the cache
@@ -594,7 +609,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
   auto v_role = [&](auto plane, int part) {
     constexpr int pl = decltype(plane)::value;
     const int w4 = warp & 3, lt = tid & 127;
-    auto v_sync = [&]() { if (pl) wg_sync(3); else if (C::NVA == 1) wg_sync(2); else wg_sync2(2); };   // the groups that share constants
+    auto v_sync = [&]() {   // the groups that share constants
+      if (pl) wg_sync(3); else if (C::NVA == 1) wg_sync(2); else wg_sync2(2);
+    };
     const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
     const int col = v_slot(lt) >> 1, hf = v_slot(lt) & 1;   // the token's place among the constants
     const int t4 = lane & 3;                                // the lane's 32 tokens: 32 t4 ..
@@ -996,7 +1013,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
           w[i] = f16x2(y[i].x, y[i].y);
         }
         *reinterpret_cast<uint4*>(prow + (((q_at / 8 + 2 * ch) ^ (slot & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(prow + (((q_at / 8 + 2 * ch + 1) ^ (slot & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+        *reinterpret_cast<uint4*>(prow + (((q_at / 8 + 2 * ch + 1) ^ (slot & 7)) << 4)) =
+            make_uint4(w[4], w[5], w[6], w[7]);
       }
       fence_async_smem();
       tc_before();
@@ -1107,7 +1125,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
                   codes2(w[k][c], v);
 #pragma unroll
                   for (int j = 0; j < 8; ++j)
-                    r[4 * (j >> 1) + 2 * k + (j & 1)] = h2u(__hfma2(u2h(v[j]), q.m[(j & 3) < 2 ? 0 : (j & 3) - 1], q.o));
+                    r[4 * (j >> 1) + 2 * k + (j & 1)] =
+                        h2u(__hfma2(u2h(v[j]), q.m[(j & 3) < 2 ? 0 : (j & 3) - 1], q.o));
                 }
               }
               tc_st_frag(lanes + ((uint32_t)(16 * hh) << 16) + (pl ? C::KR : C::KA) + 32 * c, r);
@@ -1176,7 +1195,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
 // Scores of the draft are products of BF16 numbers, exact on the 16-bit tensor cores with
 // float32 sums; its values are added in float32, as a hidden one may be infinite or NaN and must
 // not enter.  R^T is a product with both sides as two BF16 pieces (2^-16 against the result's
-// 2^-9).  The kernel is a chain of latencies: what a part needs is loaded together, ahead of it.
+// 2^-9).  The kernel is a chain of latencies: what a part needs is loaded together, ahead of it
+// (16 to 17 us cold and alone at 128 or 440 CTAs, of which a call sees what comes behind the wait).
 constexpr int kMergeThreads = 256;
 constexpr int kDraftPitch = 272;       // bytes of a staged row: rows 4 banks apart
 constexpr int kMergeChunk = 32;        // partial states whose weights are held at a time
@@ -1488,12 +1508,19 @@ cudaError_t launch_tree_t(const TreeArgs& args, int num_sms, cudaStream_t stream
     ready[dev].store(1, std::memory_order_release);
   }
   const int units = a.batch * a.g.H * a.nqb;
-  e = launch_dependent(tree_prep_kernel<D, NRES, NB>, dim3(units * (NB / 16)), dim3(256), 0, stream, a);
+  // queries a prep CTA: 16, or 32 once 16 make more CTAs than are resident at a time (R is then read half as
+  // often; 512 CTAs of 16: the call takes 123.6 us, 256 of 32: 121.3; the other way 220 CTAs 36.6 and 110 37.3 us)
+  constexpr int QP2 = NB < 32 ? NB : 32;
+  if (units * (NB / 16) > 2 * num_sms)
+    e = launch_dependent(tree_prep_kernel<D, NRES, NB, QP2>, dim3(units * (NB / QP2)), dim3(256), 0, stream, a);
+  else
+    e = launch_dependent(tree_prep_kernel<D, NRES, NB, 16>, dim3(units * (NB / 16)), dim3(256), 0, stream, a);
   if (e != cudaSuccess) return e;
   e = launch_dependent(kern, dim3(num_sms), dim3(kTreeThreads), (size_t)C::SMEM, stream, a);
   if (e != cudaSuccess) return e;
   // queries a merge CTA: 8, or 16 once that still leaves every SM several CTAs (R^T and the draft are
-  // then read half as often)
+  // then read half as often: 512 CTAs 121 us a call, against 130 with 1024 of 8; but 64 CTAs of 16 take 66 us, 128 of
+  // 8 54 us)
   const int bh = a.batch * a.g.H;
   if (bh * ((a.M + 15) / 16) >= 2 * num_sms)
     return launch_dependent(tree_merge_kernel<D, NRES, NB, 16>, dim3(bh * ((a.M + 15) / 16)), dim3(kMergeThreads), 0,
