@@ -7,15 +7,16 @@
 // layer and group: L * G blocks of page_bytes, num_pages * page_bytes apart.
 //
 // Planning is one CTA's latency (5 to 7 us for 32 rows or 256 pages), copying is bound by memory: 24
-// pages of 9.7 MB copied on write 71 us with the plan (467 MB read and written, 6.6 TB/s); 5 listed pages
-// 59 us (338 MB, 5.7 TB/s); 50 pages packed to the front 170 us (973 MB, 5.7 TB/s).
+// pages of 9.7 MB copied on write 68 us with the plan (467 MB read and written, 6.9 TB/s, a page that several rows
+// share being read from L2); 5 listed pages 57 us (338 MB, 5.9 TB/s); 50 pages packed to the front 166 us
+// (973 MB, 5.9 TB/s).
 #include "rq_internal.cuh"
 
 namespace rq {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kCopyThreads = 256;
+constexpr int kCopyThreads = 512;
 constexpr int kCopyCtasPerSm = 4;
 constexpr int kForkCols = 32;
 constexpr int kMaxForkPairs = 6144;
@@ -81,8 +82,9 @@ __device__ bool pair_ok(const CopyArgs& a, int n, int i) {
 }
 
 // The (pair, plane) blocks, cut into pieces of kPiece bytes, in one row; CTA c
-// takes a contiguous share, so that it walks along few pages.
-constexpr int kUnroll = 8;
+// takes a contiguous share, so that it walks along few pages.  2048 threads an SM with four loads in flight
+// each: 256 threads with eight take 72, 58 and 169 us in the three cases above; two loads 82, 64 and 182.
+constexpr int kUnroll = 4;
 constexpr int kPiece = kCopyThreads * kUnroll * 16;
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyArgs a) {
