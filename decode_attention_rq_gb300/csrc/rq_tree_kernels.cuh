@@ -634,7 +634,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       // Constants of this lane's token.  The anchor's coefficient c = m f, f a power of two and
       // 1 <= |m| < 2: f goes into the constants, where powers of two are exact, and m multiplies the
       // finished f (s code + o), so that a value is rounded relative to itself and not to its group's
-      // range.  That product carries 2^-7: its operands 2^-13 and m 2^6.
+      // range.  That product carries 2^-7: its operands 2^-13 and m 2^6.  Scales and offsets are
+      // multiples of 2^-9, so with f >= 1/4 subnormal operands stay exact, too; with a smaller f a value below
+      // 1/2 may be off by 2^-10, half a step of its group's offset.
       __half2 f1 = __half2half2(half_pow2(0)), f2 = f1;
       if (NRES && pl == 0) {
         uint16_t cb =

@@ -362,9 +362,10 @@ size_t rq_tree_workspace_bytes(const rq_config* cfg, int32_t batch, int32_t n_no
  *   out          device bf16 [batch][Hq][T][d]; zero for a node that sees no key
  * A K or V that a node's mask hides does not enter that node's result, not even
  * when it is infinite or NaN.  q (finite: up to 2^120 in magnitude) is scaled per
- * node by a power of two and kept in 16-bit floating point (11 significant bits), as are the rebuilt K/V and the
- * softmax weights (rebuilt K/V up to 65504); scores, softmax sums and
- * accumulators are float32.
+ * node by a power of two and kept in 16-bit floating point (11 significant bits),
+ * as are the rebuilt K/V and the softmax weights (rebuilt K/V up to 65504; a V
+ * below 1/2 with a coefficient below 1/4 to within 2^-10); scores, softmax sums
+ * and accumulators are float32.
  * With T = 1 and a mask that names the token itself this is
  * rq_decode_attention with a BF16 result.
  * Chained caches (RQ_MODE_CHAINED) are read as rq_decode_attention reads them.
@@ -506,7 +507,8 @@ typedef struct rq_rope_tensor {
  *   offsets  device int32 [batch][n] or NULL
  * The tensors need only be aligned to their element.
  * Errors: INVALID_ARG (null, bad count or config, frequencies that are not
- * finite, out strides of zero), ALIGNMENT, UNSUPPORTED (head_dim or rotary_dim outside the ranges, heads x batch > 2^30), CUDA. */
+ * finite, out strides of zero), ALIGNMENT, UNSUPPORTED (head_dim or rotary_dim
+ * outside the ranges, heads x batch > 2^30), CUDA. */
 rq_status rq_rope(const rq_rope_config* cfg, int32_t dtype, int32_t batch, int32_t n,
                   const rq_rope_tensor* q, const rq_rope_tensor* k, const int32_t* start,
                   const int32_t* offsets, void* stream);

@@ -68,6 +68,31 @@ def test_enough_queries_for_blocks_of_16_in_the_merge(d, rotation, loops):
     gpu.close()
 
 
+@pytest.mark.parametrize("alphas", [(0.2, -0.05, 0.004), (-1.5, 12.0, 1e-6)])
+def test_coefficients_far_from_one(alphas):
+    """Loops that are small, negative or large multiples of their anchor."""
+    n, T, H = 150, 6, 2
+    case = Case(L=1, P=4, G=1, H=H, d=128, g=32, B=1, Nmax=200)
+    R32, R = rotation32(128)
+    gpu = GpuCache(case, R32)
+    rng = np.random.default_rng(21)
+    base = rng.standard_normal((1, 2, 1, H, n, 128))
+    loops = [a * base + 0.02 * rng.standard_normal(base.shape) for a in alphas] + [base]
+    kvb = torch.from_numpy(np.concatenate(loops).astype(np.float32)).to(torch.bfloat16)
+    geom = oracle.Geometry(1, 4, 1, H, 128, 32, 1, 200)
+    obuf = np.zeros(geom.total_bytes, dtype=np.uint8)
+    gpu.append(0, 0, kvb, [0])
+    oracle.append(obuf, geom, R, 0, 0, kvb.double().numpy(), np.zeros(1, dtype=np.int64))
+    see, scale = tree_masks(22, 1, T), 1 / math.sqrt(128)
+    for loop in range(3):
+        qb, q = bf16(rng, 1, H, T, 128)
+        kb, kn = bf16(rng, 1, H, T, 128)
+        vb, vn = bf16(rng, 1, H, T, 128)
+        out = call(gpu, 0, 0, loop, qb, kb, vb, mask_words(see), None, [n], scale)
+        check(out, reference(obuf, geom, R, case, 0, 0, loop, q, kn, vn, see, [T], [n], scale), f"loop {loop}")
+    gpu.close()
+
+
 def test_more_rows_than_a_warp():
     """70 rows, some of them empty: the work's split over rows is summed 32 at a time."""
     B, T = 70, 3
