@@ -279,11 +279,15 @@ def rq_tree_attention(handle, layer, group, loop, batch, n_nodes, q, k_new, v_ne
     ceil(n_nodes / 64)] int64 or uint64 bits, or None (a single sequence);
     node_counts: [batch] int32 or None."""
     fn, dev = "rq_tree_attention", _device()
+    least = batch * n_nodes * 96            # one head of the smaller width
+    nq = 0 if q is None or isinstance(q, int) else q.numel()
+    nk = 0 if k_new is None or isinstance(k_new, int) else k_new.numel()
     _check(fn, lib.rq_tree_attention(
-        handle, layer, group, loop, batch, n_nodes, _arg(fn, dev, q, "bf16"), _arg(fn, dev, k_new, "bf16"),
-        _arg(fn, dev, v_new, "bf16"), _arg(fn, dev, mask, "u64", batch * n_nodes * -(-n_nodes // 64)),
+        handle, layer, group, loop, batch, n_nodes, _arg(fn, dev, q, "bf16", least),
+        _arg(fn, dev, k_new, "bf16", least), _arg(fn, dev, v_new, "bf16", nk),
+        _arg(fn, dev, mask, "u64", batch * n_nodes * -(-n_nodes // 64)),
         _arg(fn, dev, node_counts, "i32", batch), _arg(fn, dev, seq_lens, "i32", batch), softmax_scale,
-        _arg(fn, dev, out, "bf16"), _arg(fn, dev, workspace, "u8", workspace_bytes), workspace_bytes,
+        _arg(fn, dev, out, "bf16", nq), _arg(fn, dev, workspace, "u8", workspace_bytes), workspace_bytes,
         _stream(stream)))
 
 

@@ -276,12 +276,16 @@ def test_tree_refusals():
     fails(INVALID, q=q.cpu())
     fails(INVALID, out=out.float())
     fails(INVALID, q=q.transpose(1, 2))
+    fails(INVALID, out=out[:1])
+    fails(INVALID, v_new=v[:1])
+    fails(INVALID, q=q[0, 0, 0])
     fails(INVALID, mask=mask[:1])
     fails(INVALID, seq_lens=sl[:1])
     fails(INVALID, node_counts=sl.long())
     fails(INVALID, workspace=ws[:-16])
     fails(WORKSPACE, workspace_bytes=size - 1)
-    fails(UNSUPPORTED, n_nodes=257, mask=None)
+    fails(INVALID, n_nodes=128, mask=None)      # longer than the tensors
+    fails(UNSUPPORTED, n_nodes=257, mask=None, q=q.data_ptr(), k_new=k.data_ptr(), v_new=v.data_ptr())
     fails(CAPACITY, batch=3, mask=None, seq_lens=sl.data_ptr())
     for name, x in (("q", q), ("k_new", k), ("v_new", v), ("mask", mask), ("seq_lens", sl), ("out", out)):
         fails(ALIGN, **{name: x.data_ptr() + 4})
