@@ -631,23 +631,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
       // the step's table: the one before is still in use; with a single one, wait until it is not
       uint8_t* tab = tabs + (C::TABS == 2 ? (it & 1) * C::TAB : 0);
       if (C::TABS == 1) v_sync();
-      // Constants of this lane's token.  The anchor's coefficient c = m f, f a power of two and
-      // 1 <= |m| < 2: f goes into the constants, where powers of two are exact, and m multiplies the
-      // finished f (s code + o), so that a value is rounded relative to itself and not to its group's
-      // range.  That product carries 2^-7: its operands 2^-13 and m 2^6.  Scales and offsets are
-      // multiples of 2^-9, so with f >= 1/4 subnormal operands stay exact, too; with a smaller f a value below
-      // 1/2 may be off by 2^-10, half a step of its group's offset.
+      // Constants of this lane's token.  The anchor's coefficient c = m f, f a power of two: f goes into the
+      // constants, where powers of two are exact, and m multiplies the finished f (s code + o), so that a value is
+      // rounded relative to itself and not to its group's range.  That product carries 2^-7: its operands 2^-13 and m
+      // 2^6.  The multiplier s 2^7 f has to stay below 2^16, and s goes to 448: f <= 1, so that 1 <= |m| < 2 only for
+      // |c| < 2, and m takes the larger powers of two, up to |m| < 2^10.  Beyond that f grows again: V is finite
+      // while s f < 2^9, that is while |c| s < 2^18.  Scales and offsets are multiples of 2^-9, so with f >= 1/4
+      // subnormal operands stay exact, too; with a smaller f a value below 1/2 may be off by 2^-10: its own half step and
+      // its group's offset's, 2^-25 each against 2^-13 and |m| < 2 (1.25 * 2^-10 where f is two factors: the offset rounds
+      // twice).
       __half2 f1 = __half2half2(half_pow2(0)), f2 = f1;
       if (NRES && pl == 0) {
         uint16_t cb =
             *reinterpret_cast<const uint16_t*>(s + C::RV + tau * C::R_TILE + C::R_CODES + C::META + tok * 2);
         if ((cb & 0x7F80) == 0 || !on) cb = 0;                          // a subnormal c counts as zero
         const int e = (cb >> 7) & 0xFF;
-        // 4 f = 2^(e - 125) as two factors of f16 range; infinite and NaN c keep f = 1
-        const int x = (e == 0 || e == 255 ? 0 : e - 127) + 2, x1 = min(max(x, -14), 15), x2 = min(max(x - x1, -14), 15);
+        const bool plain = e != 0 && e != 255;                          // infinite and NaN c keep f = 1
+        const int up = plain ? min(max(e - 127, 0), 9) : 0;             // m = 2^up times c's sign and significand
+        // 4 f = 2^x as two factors of f16 range
+        const int x = plain ? e - 125 - up : 2, x1 = min(max(x, -14), 15), x2 = min(max(x - x1, -14), 15);
         f1 = __half2half2(half_pow2(x1));
         f2 = __half2half2(half_pow2(x2));
-        const uint32_t m = e == 255 || e == 0 ? cb : (cb & 0x807Fu) | 0x3F80u;   // c's sign and significand
+        const uint32_t m = plain ? (cb & 0x807Fu) | (uint32_t)(127 + up) << 7 : cb;
         *reinterpret_cast<__half*>(tab + PL * NG * 512 + col * 4 + hf * 2) =
             __float2half_rn(bf16_bits_to_f32(m) * 64.f);
       }

@@ -363,9 +363,11 @@ size_t rq_tree_workspace_bytes(const rq_config* cfg, int32_t batch, int32_t n_no
  * A K or V that a node's mask hides does not enter that node's result, not even
  * when it is infinite or NaN.  q (finite: up to 2^120 in magnitude) is scaled per
  * node by a power of two and kept in 16-bit floating point (11 significant bits),
- * as are the rebuilt K/V and the softmax weights (rebuilt K/V up to 65504; a V
- * below 1/2 with a coefficient below 1/4 to within 2^-10); scores, softmax sums
- * and accumulators are float32.
+ * as are the rebuilt K/V and the softmax weights; scores, softmax sums and
+ * accumulators are float32.  The rebuilt V may be up to 65504 in magnitude.  (Beyond
+ * what rq_append makes of such V: in a residual loop of a shared-anchor cache |c| times
+ * a V group's scale has to stay below 2^18.)  A V below 1/2 with a coefficient below
+ * 1/4 is met to within 1.25 * 2^-10; there a coefficient below 2^-126 counts as zero.
  * With T = 1 and a mask that names the token itself this is
  * rq_decode_attention with a BF16 result.
  * Chained caches (RQ_MODE_CHAINED) are read as rq_decode_attention reads them.
