@@ -162,12 +162,22 @@ def rq_cache_bytes(cfg: rq_config) -> int:
     return lib.rq_cache_bytes(ctypes.byref(cfg))
 
 
+# What the calls below need of a handle's cache to tell whether a tensor is long enough:
+# handle -> (KV heads, query heads, head width, rows, pages; contiguous: 0 pages)
+_caches = {}
+
+
+def _keep(handle, cfg, pages):
+    _caches[handle] = (cfg.num_heads, cfg.num_query_heads or cfg.num_heads, cfg.head_dim, cfg.max_batch, pages)
+    return handle
+
+
 def rq_cache_create(cfg: rq_config, dev_buf, nbytes: int, R_dev) -> int:
     """Returns the opaque handle (int)."""
     h = _p()
     _check("rq_cache_create", lib.rq_cache_create(ctypes.byref(cfg), _ptr(dev_buf), nbytes, _ptr(R_dev),
                                                   ctypes.byref(h)))
-    return h.value
+    return _keep(h.value, cfg, 0)
 
 
 def rq_cache_paged_bytes(cfg: rq_config, num_pages: int) -> int:
@@ -182,10 +192,11 @@ def rq_cache_create_paged(cfg: rq_config, num_pages: int, pool, nbytes: int, blo
     _check("rq_cache_create_paged", lib.rq_cache_create_paged(
         ctypes.byref(cfg), num_pages, _ptr(pool), nbytes, _ptr(block_table), max_tiles_per_row, _ptr(R_dev),
         ctypes.byref(h)))
-    return h.value
+    return _keep(h.value, cfg, num_pages)
 
 
 def rq_cache_destroy(handle: int) -> None:
+    _caches.pop(handle, None)     # first: once it is destroyed, another thread may be given the same address
     _check("rq_cache_destroy", lib.rq_cache_destroy(handle))
 
 
@@ -255,16 +266,21 @@ def _device():
     return _torch.cuda.current_device()
 
 
-def _arg(fn, dev, x, kind, count=0):
+def _arg(fn, dev, x, kind, count):
     """Address of x for a C call.  None and ints (device addresses) pass as they
     are; a tensor has to be contiguous, of the kind's dtype, on device dev (the one
-    current on this thread) and at least `count` long (0: the call's arguments do not
-    tell the length): a host pointer or a short buffer would fault the device."""
+    current on this thread) and at least `count` long: a host pointer or a short buffer
+    would fault the device."""
     if x is None or isinstance(x, int):
         return x
     if x.dtype not in _DT[kind] or x.get_device() != dev or x.numel() < count or not x.is_contiguous():
         raise RqError(fn, 1)
     return x.data_ptr()
+
+
+def _pages(handle):
+    """Pages of the handle's cache: the length of refs."""
+    return _caches.get(handle, (0,) * 5)[4]
 
 
 def rq_tree_workspace_bytes(cfg: rq_config, batch: int, n_nodes: int) -> int:
@@ -279,12 +295,17 @@ def rq_tree_attention(handle, layer, group, loop, batch, n_nodes, q, k_new, v_ne
     ceil(n_nodes / 64)] int64 or uint64 bits, or None (a single sequence);
     node_counts: [batch] int32 or None."""
     fn, dev = "rq_tree_attention", _device()
-    least = batch * n_nodes * 96            # one head of the smaller width
-    nq = 0 if q is None or isinstance(q, int) else q.numel()
-    nk = 0 if k_new is None or isinstance(k_new, int) else k_new.numel()
+    cache = _caches.get(handle)
+    if cache is None:     # a handle made without this binding: one head of the smaller width, out as q, v_new as k_new
+        nq, nk = (max(batch * n_nodes * 96, 0 if x is None or isinstance(x, int) else x.numel()) for x in (q, k_new))
+    elif batch > cache[3] or n_nodes > RQ_MAX_TREE_NODES:     # the library refuses these before it reads anything
+        nq = nk = 0
+    else:
+        nodes = batch * n_nodes * cache[2]
+        nk, nq = nodes * cache[0], nodes * cache[1]
     _check(fn, lib.rq_tree_attention(
-        handle, layer, group, loop, batch, n_nodes, _arg(fn, dev, q, "bf16", least),
-        _arg(fn, dev, k_new, "bf16", least), _arg(fn, dev, v_new, "bf16", nk),
+        handle, layer, group, loop, batch, n_nodes, _arg(fn, dev, q, "bf16", nq),
+        _arg(fn, dev, k_new, "bf16", nk), _arg(fn, dev, v_new, "bf16", nk),
         _arg(fn, dev, mask, "u64", batch * n_nodes * -(-n_nodes // 64)),
         _arg(fn, dev, node_counts, "i32", batch), _arg(fn, dev, seq_lens, "i32", batch), softmax_scale,
         _arg(fn, dev, out, "bf16", nq), _arg(fn, dev, workspace, "u8", workspace_bytes), workspace_bytes,
@@ -307,8 +328,8 @@ def rq_pages_fork(handle, n, src_rows, dst_rows, refs, status=None, stream=None)
     """Row dst_rows[i] shares the pages of row src_rows[i] and gives up its own."""
     fn, dev = "rq_pages_fork", _device()
     _check(fn, lib.rq_pages_fork(
-        handle, n, _arg(fn, dev, src_rows, "i32", n), _arg(fn, dev, dst_rows, "i32", n), _arg(fn, dev, refs, "i32"),
-        _arg(fn, dev, status, "i32", 4), _stream(stream)))
+        handle, n, _arg(fn, dev, src_rows, "i32", n), _arg(fn, dev, dst_rows, "i32", n),
+        _arg(fn, dev, refs, "i32", _pages(handle)), _arg(fn, dev, status, "i32", 4), _stream(stream)))
 
 
 def rq_pages_reserve(handle, batch, seq_lens, n_tokens, refs, status, workspace, workspace_bytes, stream=None):
@@ -316,7 +337,8 @@ def rq_pages_reserve(handle, batch, seq_lens, n_tokens, refs, status, workspace,
     (copy on write where a page is shared)."""
     fn, dev = "rq_pages_reserve", _device()
     _check(fn, lib.rq_pages_reserve(
-        handle, batch, _arg(fn, dev, seq_lens, "i32", batch), n_tokens, _arg(fn, dev, refs, "i32"),
+        handle, batch, _arg(fn, dev, seq_lens, "i32", batch), n_tokens,
+        _arg(fn, dev, refs, "i32", _pages(handle)),
         _arg(fn, dev, status, "i32", 4), _arg(fn, dev, workspace, "u8", workspace_bytes), workspace_bytes,
         _stream(stream)))
 
@@ -325,7 +347,8 @@ def rq_pages_free(handle, n, rows, keep, refs, status=None, stream=None):
     """Give up the pages of rows[i] behind its first keep[i] tokens (keep None: all)."""
     fn, dev = "rq_pages_free", _device()
     _check(fn, lib.rq_pages_free(
-        handle, n, _arg(fn, dev, rows, "i32", n), _arg(fn, dev, keep, "i32", n), _arg(fn, dev, refs, "i32"),
+        handle, n, _arg(fn, dev, rows, "i32", n), _arg(fn, dev, keep, "i32", n),
+        _arg(fn, dev, refs, "i32", _pages(handle)),
         _arg(fn, dev, status, "i32", 4), _stream(stream)))
 
 
@@ -334,8 +357,9 @@ def rq_pages_compact(handle, refs, used, status, workspace, workspace_bytes, str
     receives their number."""
     fn, dev = "rq_pages_compact", _device()
     _check(fn, lib.rq_pages_compact(
-        handle, _arg(fn, dev, refs, "i32"), _arg(fn, dev, used, "i32", 1), _arg(fn, dev, status, "i32", 4),
-        _arg(fn, dev, workspace, "u8", workspace_bytes), workspace_bytes, _stream(stream)))
+        handle, _arg(fn, dev, refs, "i32", _pages(handle)), _arg(fn, dev, used, "i32", 1),
+        _arg(fn, dev, status, "i32", 4), _arg(fn, dev, workspace, "u8", workspace_bytes), workspace_bytes,
+        _stream(stream)))
 
 
 def rq_rope(cfg: rq_rope_config, q, k, start, offsets=None, q_out=None, k_out=None, stream=None):
