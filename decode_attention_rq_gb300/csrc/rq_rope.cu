@@ -13,7 +13,9 @@
 // Memory-bound: every element is read and written once.  537 MB (8192 tokens, 4 rows, 32 heads of 128, BF16)
 // take 85 us, 6.3 TB/s; 172 MB of float32 (1021 tokens, 2 rows, 110 heads of 96) 33 us, 5.2 TB/s, of which some
 // 6 us are a launch's start and end.  A token's call (n = 1) is a launch's latency.
+#include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include <cuda_fp16.h>
 
@@ -260,6 +262,48 @@ cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// Whether two of the tensor's results, of d channels each, share an element: whether some step (i, j, k), not
+// all zero, along its axes leads less than d elements away.  Axes sorted by stride: where each one steps
+// over all that lies inside it, as in ordinary layouts, none does.  Otherwise (axes that interlock) the steps along
+// the two longer strides are tried as far as the shortest axis could lead back from them.
+bool results_overlap(const int64_t (&size)[3], const int64_t (&stride)[3], int d) {
+  using wide = __int128;
+  wide n[3] = {0, 0, 0}, s[3] = {1, 1, 1};     // last steps (0: an axis not in use), lengths of a step
+  for (int i = 0; i < 3; ++i)
+    if (size[i] > 1) {
+      n[i] = size[i] - 1;
+      s[i] = stride[i] < 0 ? -(wide)stride[i] : (wide)stride[i];
+    }
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if ((n[j] ? s[j] : 0) > (n[j + 1] ? s[j + 1] : 0)) {
+        std::swap(n[j], n[j + 1]);
+        std::swap(s[j], s[j + 1]);
+      }
+  wide inside = d;
+  bool nested = true;
+  for (int i = 0; i < 3; ++i)
+    if (n[i]) {
+      nested = nested && s[i] >= inside;
+      inside += n[i] * s[i];
+    }
+  if (nested) return false;
+  for (wide k = 0; k <= n[2] && k * s[2] < n[1] * s[1] + n[0] * s[0] + d; ++k) {
+    // j s1 within reach of -k s2: n0 s0 + d away at most
+    const wide reach = n[0] * s[0] + d;
+    const wide j0 = std::max((-k * s[2] - reach) / s[1], -n[1]), j1 = std::min((reach - k * s[2]) / s[1], n[1]);
+    for (wide j = k ? j0 : 0; j <= j1; ++j) {   // k = 0: a step and its opposite are alike
+      // the steps along the shortest axis that lead nearest
+      const wide at = k * s[2] + j * s[1], back = std::clamp(-at / s[0], -n[0], n[0]);
+      for (wide i = std::max(back - 1, -n[0]); i <= std::min(back + 1, n[0]); ++i) {
+        const wide gap = at + i * s[0];
+        if ((i || j || k) && gap < d && gap > -(wide)d) return true;
+      }
+    }
+  }
+  return false;
+}
+
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 }  // namespace
@@ -293,8 +337,11 @@ extern "C" rq_status rq_rope(const rq_rope_config* cfg, int32_t dtype, int32_t b
       return RQ_ERR_INVALID_ARG;
     heads += x->heads;
   }
-  if (!aligned_to(start, 4) || !aligned_to(offsets, 4)) return RQ_ERR_ALIGNMENT;
   if (heads * (batch > 0 ? batch : 1) > (1 << 30)) return RQ_ERR_UNSUPPORTED;
+  for (const rq_rope_tensor* x : {q, k})
+    if (x && batch > 0 && n > 0 && results_overlap({batch, x->heads, n}, {x->out_row, x->out_head, x->out_token}, d))
+      return RQ_ERR_INVALID_ARG;
+  if (!aligned_to(start, 4) || !aligned_to(offsets, 4)) return RQ_ERR_ALIGNMENT;
   if (batch == 0 || n == 0) return RQ_OK;
 
   RopeArgs a = {};

@@ -485,8 +485,9 @@ typedef struct rq_rope_config {
 /* One tensor [batch][heads][n][d] read and written by rq_rope: the element
  * strides of row, head and token; channels are contiguous.  Any strides do;
  * pointers and strides that are multiples of 16 bytes are faster.  out's elements
- * are distinct (a stride of zero over several rows, heads or tokens is refused).
- * out may be in (with the same strides); otherwise the two must not overlap. */
+ * are distinct (strides that put two results of it in one place are refused).
+ * out may be in (with the same strides); otherwise the two must not overlap, nor
+ * q's out and k's, nor either's out and the other's in: these are not checked. */
 typedef struct rq_rope_tensor {
   const void* in;
   void* out;
@@ -509,7 +510,7 @@ typedef struct rq_rope_tensor {
  *   offsets  device int32 [batch][n] or NULL
  * The tensors need only be aligned to their element.
  * Errors: INVALID_ARG (null, bad count or config, frequencies that are not
- * finite, out strides of zero), ALIGNMENT, UNSUPPORTED (head_dim or rotary_dim
+ * finite, results of one tensor that overlap), ALIGNMENT, UNSUPPORTED (head_dim or rotary_dim
  * outside the ranges, heads x batch > 2^30), CUDA. */
 rq_status rq_rope(const rq_rope_config* cfg, int32_t dtype, int32_t batch, int32_t n,
                   const rq_rope_tensor* q, const rq_rope_tensor* k, const int32_t* start,
