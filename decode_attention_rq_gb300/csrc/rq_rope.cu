@@ -355,6 +355,7 @@ extern "C" rq_status rq_rope(const rq_rope_config* cfg, int32_t dtype, int32_t b
   const double kTwoPi = 6.283185307179586476925;
   double theta = cfg->theta;
   if (cfg->scaling == RQ_ROPE_BASE) theta *= std::pow(cfg->factor, (double)r / (r - 2));
+  if (!std::isfinite(theta)) return RQ_ERR_INVALID_ARG;   // every pair but the first would stand still
   const double ratio = std::pow(theta, -2.0 / r);
   double f = 1.0;
   for (int j = 0; j < r / 2; ++j, f *= ratio) {

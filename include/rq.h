@@ -509,8 +509,8 @@ typedef struct rq_rope_tensor {
  *   start    device int32 [batch], or NULL: zeros
  *   offsets  device int32 [batch][n] or NULL
  * The tensors need only be aligned to their element.
- * Errors: INVALID_ARG (null, bad count or config, frequencies that are not
- * finite, results of one tensor that overlap), ALIGNMENT, UNSUPPORTED (head_dim or rotary_dim
+ * Errors: INVALID_ARG (null, bad count or config, a stretched base or frequencies not
+ * finite in float64, results of one tensor that overlap), ALIGNMENT, UNSUPPORTED (head_dim or rotary_dim
  * outside the ranges, heads x batch > 2^30), CUDA. */
 rq_status rq_rope(const rq_rope_config* cfg, int32_t dtype, int32_t batch, int32_t n,
                   const rq_rope_tensor* q, const rq_rope_tensor* k, const int32_t* start,
