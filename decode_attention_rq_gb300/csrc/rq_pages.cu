@@ -82,8 +82,9 @@ __device__ bool pair_ok(const CopyArgs& a, int n, int i) {
 }
 
 // The (pair, plane) blocks, cut into pieces of kPiece bytes, in one row; CTA c
-// takes a contiguous share, so that it walks along few pages.  2048 threads an SM with four loads in flight
-// each: 256 threads with eight take 72, 58 and 169 us in the three cases above; two loads 82, 64 and 182.
+// takes a contiguous share, so that it walks along few pages.  Four loads in flight a thread; at 45 registers two of
+// the grid's four CTAs an SM run at a time, 1024 threads.  256 threads with eight loads take 72, 58 and 169 us in
+// the three cases above; two loads 82, 64 and 182.
 constexpr int kUnroll = 4;
 constexpr int kPiece = kCopyThreads * kUnroll * 16;
 

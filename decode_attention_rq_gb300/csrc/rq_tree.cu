@@ -19,8 +19,9 @@ __device__ __forceinline__ float2 meta2(const uint8_t* p) {   // (scale, offset)
 // ---- one CTA per (node, query head, row) -------------------------------------
 // The path of chained caches, whose planes fold into one another and so do not make a matrix product of
 // two parts.  Dequantizes every key and value for its one query: the CTAs of one KV head read the same tiles
-// from L2.  Bound by that arithmetic, not by memory: on a shared-anchor cache (16 heads, 8192
-// tokens, 4 rows of 16 nodes) it took 5214 us, against 54 of the tensor-core path.
+// from L2.  Bound by that arithmetic, not by memory: 16 heads of 128, 8192 tokens, 4 rows of 16 nodes take 5206 us with one
+// residual plane to read and 9619 with three (one node a row: 4746); the tensor-core path takes 54 on a
+// shared-anchor cache.
 constexpr int kRowThreads = 128;
 constexpr int kMaxPlanes = kMaxLoops;      // anchor + residual planes a call reads
 

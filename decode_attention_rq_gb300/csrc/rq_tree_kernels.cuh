@@ -21,8 +21,8 @@
 // Dequantization: an f16 whose bits are an integer n < 1024 has the value n 2^-24, so masking a
 // code word leaves codes times 2^(p - 24), p the field's first bit; one fused multiply-add with
 // (s 2^(24 - p - k), o 2^-k) gives (s code + o) 2^-k.  k = 15: every E4M3 s and o stays in f16's
-// range, and being multiples of 2^-9 they and the sums stay exact.  (Logic and shift instructions
-// run at half rate here and bound this kernel: 7 of them a word of 8 codes, 11 of 16.)
+// range and, being a multiple of 2^-9, exact; s code + o, below 4 exact, too, is rounded to 11 bits above.  (Logic
+// and shift instructions run at half rate here and bound this kernel: 7 of them a word of 8 codes, 11 of 16.)
 //
 // Softmax: a token's scores sit in one lane, a query's across the lanes.  The running
 // reference of a query therefore moves only when some score exceeds it by 2^8 (the first
@@ -1204,6 +1204,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_mma_kernel(TreeArgs a) {
 // not enter.  R^T is a product with both sides as two BF16 pieces (2^-16 against the result's
 // 2^-9).  The kernel is a chain of latencies: what a part needs is loaded together, ahead of it
 // (16 to 17 us cold and alone at 128 or 440 CTAs, of which a call sees what comes behind the wait).
+// The 16-query instances do not fit their 64 registers: 44 to 144 bytes a thread are spilled and 268 to 416 reloaded (the
+// 8-query ones 8 to 32 of each).
 constexpr int kMergeThreads = 256;
 constexpr int kDraftPitch = 272;       // bytes of a staged row: rows 4 banks apart
 constexpr int kMergeChunk = 32;        // partial states whose weights are held at a time

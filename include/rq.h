@@ -429,7 +429,8 @@ rq_status rq_pages_fork(rq_cache* cache, int32_t n, const int32_t* src_rows, con
  * its bytes when the tile already holds tokens of the row (copy on write).  When
  * every holder of a page asks in one call, the last of them keeps it.  Requests are
  * served in row, then tile order, from the lowest free page up.  Where the free
- * pages run out an entry stays as it is (status [3]).  A row with a negative
+ * pages run out an entry stays as it is (status [3]): pages may then still be shared
+ * by rows that asked, and no row may be written to before a reserve has succeeded.  A row with a negative
  * length or seq_lens[b] + n_tokens > max_seq_len is skipped (status [1]).  n_tokens = 0 does
  * nothing. */
 rq_status rq_pages_reserve(rq_cache* cache, int32_t batch, const int32_t* seq_lens, int32_t n_tokens,
@@ -463,7 +464,9 @@ typedef enum rq_rope_scaling {
                            is divided by `factor`, the fastest stays */
   RQ_ROPE_PARTS = 3     /* f_i (k_i + (1 - k_i) / factor), k_i = clamp((u_i - low_turns) /
                            (high_turns - low_turns), 0, 1), u_i = original_len f_i / 2pi: the turns
-                           that pair i makes over the original length */
+                           that pair i makes over the original length.  The ramp is linear in the
+                           turns; models trained with one that is linear in the pair's index i,
+                           between two bounds rounded to indices, have other frequencies */
 } rq_rope_scaling;
 
 /* How rq_rope turns a head. */
@@ -510,8 +513,8 @@ typedef struct rq_rope_tensor {
  *   offsets  device int32 [batch][n] or NULL
  * The tensors need only be aligned to their element.
  * Errors: INVALID_ARG (null, bad count or config, a stretched base or frequencies not
- * finite in float64, results of one tensor that overlap), ALIGNMENT, UNSUPPORTED (head_dim or rotary_dim
- * outside the ranges, heads x batch > 2^30), CUDA. */
+ * finite in float64, results of one tensor that overlap), ALIGNMENT, UNSUPPORTED
+ * (head_dim or rotary_dim outside the ranges, heads x batch > 2^30), CUDA. */
 rq_status rq_rope(const rq_rope_config* cfg, int32_t dtype, int32_t batch, int32_t n,
                   const rq_rope_tensor* q, const rq_rope_tensor* k, const int32_t* start,
                   const int32_t* offsets, void* stream);
