@@ -370,7 +370,9 @@ size_t rq_tree_workspace_bytes(const rq_config* cfg, int32_t batch, int32_t n_no
  * 1/4 is met to within 1.25 * 2^-10; there a coefficient below 2^-126 counts as zero.
  * With T = 1 and a mask that names the token itself this is
  * rq_decode_attention with a BF16 result.
- * Chained caches (RQ_MODE_CHAINED) are read as rq_decode_attention reads them.
+ * Chained caches (RQ_MODE_CHAINED) are read as rq_decode_attention reads them, but
+ * node by node: a call takes about a hundred times what it takes on a shared-anchor
+ * cache, so a single token there is better served by rq_decode_attention.
  * Errors: as rq_decode_attention; INVALID_ARG (n_nodes < 1), UNSUPPORTED
  * (n_nodes > RQ_MAX_TREE_NODES, batch > RQ_MAX_DECODE_BATCH, more than 2^30
  * queries, batch * H * ceil(Hq / H * T / 64) * ceil(max_seq_len / 128) > 2^31 - 1). */
