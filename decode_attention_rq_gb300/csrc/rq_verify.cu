@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) verify_kernel(VerifyArgs a)
   __shared__ int token_s[RQ_MAX_TREE_NODES], parent_s[RQ_MAX_TREE_NODES], path_s[RQ_MAX_TREE_NODES];
   __shared__ float left_s[RQ_MAX_TREE_NODES], q_s[RQ_MAX_TREE_NODES], u_s[RQ_MAX_TREE_NODES];   // r and q at the node's token
   __shared__ unsigned long long words_s[2][kMaxCluster * kVerifyWarps];
+  __shared__ float base_s[kMaxCluster * kVerifyWarps];      // segments' sums when last added up
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ranks = cluster_size(), rank = cluster_rank();
   const int b = blockIdx.x / ranks, T_ = a.T;
@@ -360,6 +361,22 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) verify_kernel(VerifyArgs a)
     }
     m.meet(warp_sum(s).word());
     total = m.sum();
+    if (tid < kMaxCluster * kVerifyWarps) base_s[tid] = sum_of(m.met()[tid]).h;   // read behind a barrier
+  };
+  // Segment `at` summed as in a pass, from r_s; every warp's word goes round again.
+  auto resum = [&](int at) {
+    unsigned long long word = m.met()[rank * kVerifyWarps + warp];
+    if (at == (int)rank * kVerifyWarps + warp) {
+      const int stop = min(skew + nv, (warp + 1) * seg);
+      Sum2 s;
+      for (int j = warp * seg + lane * 8; j < stop; j += 256) {
+        for (int k = 0; k < 8; ++k) s.add(r_s[j + k]);
+        s.settle();
+      }
+      word = warp_sum(s).word();
+    }
+    m.meet(word);
+    if (tid == 0) base_s[at] = sum_of(m.met()[at]).h;
   };
 
   int cur = 0, count = n ? 1 : 0, pick = -1;
@@ -400,9 +417,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) verify_kernel(VerifyArgs a)
         pass(cur, fresh, a.draft != nullptr, z, a.draft ? -1 : x);
         whole = total.h;
       } else {
-        // only r(x) goes: off its segment's sum.  Summed anew once little is left, for what cancels is 2^-44 of `whole`.
+        // only r(x) goes: off its segment's sum.  All is summed anew once little is left, for what cancels is 2^-44 of
+        // `whole`; one segment once 2^-20 of its own sum is left, or an empty one could seem to hold something.
+        const int owner = x / a.slice, j = skew + x - owner * a.slice, at = owner * kVerifyWarps + j / seg;
         if (tid == 0) {
-          const int owner = x / a.slice, j = skew + x - owner * a.slice, at = owner * kVerifyWarps + j / seg;
           Sum2 s = sum_of(m.met()[at]), y;
           y.h = -rx;
           s.add(y);
@@ -410,6 +428,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) verify_kernel(VerifyArgs a)
           if (owner == (int)rank) r_s[j] = 0.f;
         }
         __syncthreads();
+        if (rx > 0.f && !(sum_of(m.met()[at]).h > 0x1p-20f * base_s[at])) resum(at);
         total = m.sum();
         if (!(total.h > 0.0625f * whole)) {
           pass(cur, false, false, z, -1);

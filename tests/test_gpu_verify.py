@@ -311,3 +311,25 @@ def test_graphs_and_calls_at_once():
             p, q, tokens, parents, accept, sample = s[1][i]
             for got in (s[3], e):
                 check([x.cpu().numpy() for x in got], s[0], p, q if s[0] == 0 else None, tokens, parents, None, accept, sample)
+
+
+@pytest.mark.parametrize("kept", [False, True])
+@pytest.mark.parametrize("V", [40, 5000, 70001])
+def test_refusals_side_by_side(V, kept):
+    """No draft distribution: siblings next to each other, their probabilities spread over 2^30, all refused, with nothing
+    or a little left beside them and half of all elsewhere.  The samples count as 0: the next token is the first of anything."""
+    import decode_attention_rq_gb300 as rq
+    B, T, at = 96, 9, V // 3
+    rng = np.random.default_rng(V)
+    p = np.zeros((B, T, V), dtype=np.float32)
+    p[:, 0, V - 1] = 0.5
+    p[:, 0, at:at + T - 1] = rng.random((B, T - 1)) * 2.0 ** -(4 + 30 * rng.random((B, T - 1)))
+    if kept:
+        p[:, 0, at + T] = 2.0 ** -(40 + 20 * rng.random(B))
+    tokens = np.full((B, T), at, dtype=np.int32)
+    for b in range(B):
+        tokens[b, 1:] += rng.permutation(T - 1).astype(np.int32)
+    parents, accept = np.zeros((B, T), dtype=np.int32), np.ones((B, T), dtype=np.float32)
+    sample = np.array([0.0, -1.0, np.nan, -0.0], dtype=np.float32)[np.arange(B) % 4]
+    p = torch.from_numpy(p)
+    check(run(rq, 0, p, None, tokens, parents, None, accept, sample), 0, p, None, tokens, parents, None, accept, sample)
