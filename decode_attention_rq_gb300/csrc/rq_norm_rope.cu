@@ -329,14 +329,14 @@ __global__ void __launch_bounds__(kNormThreads, BACK && S == 1 ? 4 : 1) norm_vec
       for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int i = 0; i < V; ++i) ss = fma2(v[k][s][i], v[k][s][i], ss);
-      sum[k] = ss.x + ss.y;
+      sum[k] = (ss.x + ss.y) * inv_d;   // a lane's share of the mean: 512 squares of 2^60 would not fit a sum
     }
 #pragma unroll
     for (int k = 0; k < KH; ++k) sum[k] = group_sum<G>(sum[k]);
     if (!BACK) {
 #pragma unroll
       for (int k = 0; k < KH; ++k) {
-        const float2 rstd = both(rsqrtf(fmaf(sum[k], inv_d, a.eps)));
+        const float2 rstd = both(rsqrtf(sum[k] + a.eps));
         const bool have = on && (k == 0 || share.head * KH + k < x.heads);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kNormThreads, BACK && S == 1 ? 4 : 1) norm_vec
         }
       const float td = group_sum<G>(dot.x + dot.y);
       // a group without a token has zeros: eps = 0 must not make its weights' sums NaN
-      const float r = on ? rsqrtf(fmaf(sum[0], inv_d, a.eps)) : 0.f;
+      const float r = on ? rsqrtf(sum[0] + a.eps) : 0.f;
       const float2 rstd = both(r), c = both(-td * inv_d * r * r);
 #pragma unroll
       for (int s = 0; s < S; ++s) {
@@ -525,8 +525,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_any_kernel(NormArgs a) {
       for (int i = 0; i < 2 * V; ++i) ss = fmaf(v[s][i], v[s][i], ss);
     }
     fetch();
-    ss = group_sum<G>(ss);
-    const float rstd = on ? rsqrtf(fmaf(ss, inv_d, a.eps)) : 0.f;
+    ss = group_sum<G>(ss * inv_d);
+    const float rstd = on ? rsqrtf(ss + a.eps) : 0.f;
     if (!BACK)
 #pragma unroll
       for (int s = 0; s < S; ++s)

@@ -638,7 +638,7 @@ typedef struct rq_norm_tensor {
  *   y = Rot(position) (w x / sqrt(mean(x^2) + eps))
  * over the head_dim channels of x; Rot, positions and configuration as rq_rope.  Arithmetic
  * is float32 (x up to 2^60 in magnitude), rounded once to the tensors' type.  With eps = 0 a vector of zeros
- * gives NaN.
+ * gives NaN; one whose largest magnitude is below 2^-50 loses accuracy then, below 2^-70 it may give infinities.
  *   weight_dtype  rq_dtype of both weights
  *   q, k          host; either may be NULL.  out may be in, as in rq_rope
  * Errors: as rq_rope; INVALID_ARG (weight_dtype, eps negative or not finite), UNSUPPORTED

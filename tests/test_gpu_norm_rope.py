@@ -306,3 +306,31 @@ def test_widths_and_rotated_parts(dtype, inter):
                 dx, dwr, bar, wbar = backward(rq, cfg, f64(z), f64(v), 1e-5, pos, f64(y))
                 close(got, dx, bar * 2.0 ** -18, dtype, f"dx {d} {r}")
                 close(gw, dwr, wbar * (2.0 ** -18 + 5 * nh * 2.0 ** -24), F, f"dw {d} {r}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("d,r", [(128, 64), (128, 58), (256, 128), (512, 256), (511, 254)])
+@pytest.mark.parametrize("top,eps", [(2.0 ** 60, 1e-6), (2.0 ** -50, 0.0)])
+def test_ends_of_the_range(dtype, d, r, top, eps):
+    """Magnitudes up to 2^60, every channel there in one head; with eps = 0 down to vectors whose largest is 2^-50."""
+    case = (dtype, F, d, r, 0, 0, 0, 1, 3, 1, 5, [9], False)
+    rq, cfg, x, w, g, _, pos = inputs(case, d)
+    x = (x.float().sign() * top * (0.5 + 0.5 * torch.rand(x.shape, generator=torch.Generator().manual_seed(d)))).to(dtype)
+    x[:, :, 0] = top
+    x[:, :, 1, 1:] = 0                               # one channel alone
+    x[:, :, 1, 0] = top
+    start, dev, dg, wd = torch.tensor([9], dtype=torch.int32).cuda(), x.cuda(), g.cuda(), [v.cuda() for v in w]
+    q, k, qg, kg = heads(dev, 0, 3), heads(dev, 3, None), heads(dg, 0, 3), heads(dg, 3, None)
+    out = torch.full_like(dev, 99)
+    rq.rq_norm_rope(cfg, q, k, *wd, eps, start, None, heads(out, 0, 3), heads(out, 3, None))
+    for got, z, v in ((heads(out, 0, 3), q, w[0]), (heads(out, 3, None), k, w[1])):
+        ref, size = forward(rq, cfg, f64(z), f64(v), eps, pos)
+        close(got, ref, size * 2.0 ** -18, dtype)
+    dw, ws = torch.full((2, d), 7.0, device="cuda"), torch.empty(rq.rq_norm_rope_workspace_bytes(d), dtype=torch.uint8,
+                                                                 device="cuda")
+    rq.rq_norm_rope_backward(cfg, q, k, qg, kg, *wd, eps, start, None, heads(out, 0, 3), heads(out, 3, None), dw[0], dw[1],
+                             ws, ws.numel())
+    for got, gw, nh, z, v, y in ((heads(out, 0, 3), dw[0], 3, q, w[0], qg), (heads(out, 3, None), dw[1], 1, k, w[1], kg)):
+        dx, dwr, bar, wbar = backward(rq, cfg, f64(z), f64(v), eps, pos, f64(y))
+        close(got, dx, bar * 2.0 ** -18, dtype, "dx")
+        close(gw, dwr, wbar * (2.0 ** -18 + 5 * nh * 2.0 ** -24), F, "dw")
