@@ -7,7 +7,7 @@
 //
 // Plan (once a step, for all layers and loops): the tiles that every family shares, found by comparing its rows' table
 // entries; each row's rest as a table and a length of its own; the split of the work.  Then a call is four launches,
-// each started early by the one before:
+// each but the first started early by the one before:
 //   1. prefix_prep_kernel: q and R q as operands of both streaming kernels.
 //   2. the tensor-core streaming kernel of rq_tree_kernels.cuh over the shared tiles: its "rows" are blocks of NB queries
 //      of a family, so that the shared tiles are read and dequantized once for NB rows.
@@ -372,7 +372,9 @@ __device__ __forceinline__ bool plan_fits(const PrefixArgs& a) {
 // 16 queries a CTA, neighbours in their family and of one KV head: as operands of the tensor-core kernel for the shared
 // tiles (their place in a block of NB), and for the row's own (OWN: their place among its query heads) or as packs of
 // the decode kernel.  x is BF16 and so exact; R x is a product on the 16-bit tensor cores, R as two BF16 pieces
-// (2^-16) from the plan.  All of it comes ahead of the wait: only the copy to the workspace follows.
+// (2^-16) from the plan.  Only the plan is read ahead of the wait (its last kernel releases no dependents early): the
+// kernel before the call may release its own early and write queries, tokens or the cache.  The call's other kernels start
+// behind this wait and may read them at once.
 template <int D, int GS, int NRES, int NB, bool OWN>
 __global__ void __launch_bounds__(256) prefix_prep_kernel(PrefixArgs a) {
   using C = Cfg<D, GS, NRES>;
@@ -388,7 +390,6 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(PrefixArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const bool hadamard = (a.g.mode & RQ_MODE_HADAMARD) != 0;
   const int part = blockIdx.x / a.g.H, h = blockIdx.x % a.g.H;
-  pdl_launch_dependents();
   const bool fits = plan_fits(a);
   const int4 rec = __ldg(reinterpret_cast<const int4*>(a.plan + a.l.prep) + part);
   const int row0 = rec.x, first = rec.y, queries = rec.z, block0 = rec.w, valid = min(kPrepQ, queries - first);
@@ -401,10 +402,9 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(PrefixArgs a) {
       rf[NRES ? k : 0][1] = __ldg(rp + k * 64 + 1);
     }
   }
-  if (!fits || row0 < 0) {
-    pdl_wait();
-    return;
-  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!fits || row0 < 0) return;
   // one warp per query: its values (zeros where there is none), its power of two
 #pragma unroll
   for (int r = warp; r < kPrepQ; r += 8) {
@@ -547,7 +547,6 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(PrefixArgs a) {
     }
   }
   __syncthreads();
-  pdl_wait();
   // 16 channels make a block of 32 bytes a query, swizzled by the query's place
   auto at = [](int row, int c, int nb) { return ((c >> 1) * nb + row) * 32 + (((c & 1) ^ ((row >> 2) & 1)) << 4); };
   if (block0 >= 0) {
@@ -587,7 +586,8 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(PrefixArgs a) {
 // One CTA per MQ queries of a family and KV head: neighbours in the block, so that the shared tiles' partial states (four
 // queries to 16 bytes) are read whole.  256 threads: a channel's anchor part below, its residual part above; a warp takes a
 // query's (MQ = 16: two queries') score, maxima and weights.  R^T comes into shared memory by one bulk copy, ahead of
-// the wait.  A chain of latencies: states' references, weights, accumulators, R^T: 6.3 us behind the wait in the header's
+// the wait.  Dependents are not released early: a decode call, which reads its queries ahead of its wait, may take `out`
+// for them.  A chain of latencies: states' references, weights, accumulators, R^T: 6.3 us behind the wait in the header's
 // case (9 with addresses computed in its loops and R^T read from the L2 by each warp).
 constexpr int kWeights = 32;              // states whose weights are held at a time
 template <int D, int NRES, int NB, int MQ, bool OWN>
@@ -606,7 +606,6 @@ __global__ void __launch_bounds__(256, 2) prefix_merge_kernel(PrefixArgs a) {
   const int g = lane >> 2, t4 = lane & 3;
   const int m = blockIdx.x / a.g.H, h = blockIdx.x % a.g.H;
   const bool hadamard = (a.g.mode & RQ_MODE_HADAMARD) != 0, dense = NRES && !hadamard;
-  pdl_launch_dependents();
   const bool fits = plan_fits(a);
   const int4 rec = __ldg(reinterpret_cast<const int4*>(a.plan + a.l.merge) + 2 * m);
   const int4 work = __ldg(reinterpret_cast<const int4*>(a.plan + a.l.merge) + 2 * m + 1);

@@ -25,7 +25,9 @@
  *     dependents) has completed before a call starts, so any such kernel may
  *     write the inputs; a kernel that does release early must not be the one
  *     that writes them (its writes are visible only to a kernel that has
- *     waited for it).
+ *     waited for it).  rq_tree_attention and rq_prefix_attention wait before
+ *     they read inputs, so any kernel may write theirs, and their results may
+ *     be a decode call's inputs.
  *   - Argument errors are found on the host before anything is enqueued and
  *     return a status; nothing is launched then.  A failed launch returns
  *     RQ_ERR_CUDA.  Faults inside a kernel surface on a later CUDA call.
