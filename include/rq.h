@@ -499,7 +499,8 @@ size_t rq_prefix_workspace_bytes(const rq_config* cfg, int32_t batch, int32_t n_
  *   out               device bf16 [batch][Hq][d]
  * Over shared tiles the rounding and the ranges of V are rq_tree_attention's (K, V and softmax weights to 11 bits,
  * float32 sums); over a row's own tiles they are, too, for caches of 3 to 16 query heads per KV head, and otherwise
- * rq_decode_attention's.
+ * rq_decode_attention's.  A dense rotation is multiplied as two BF16 pieces on every path: R is off by up to 2^-18 of
+ * each element in R q (a score by some 2^-18 |R q| |r| scale), the sums of R^T by up to 2^-16 of their magnitudes.
  * Errors: as rq_prefix_plan; WORKSPACE (plan or workspace too small). */
 rq_status rq_prefix_attention(rq_cache* cache, int32_t layer, int32_t group, int32_t loop, int32_t batch,
                               int32_t n_prefixes, const void* plan, size_t plan_bytes, const void* q,
