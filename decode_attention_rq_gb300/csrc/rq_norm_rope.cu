@@ -702,6 +702,10 @@ rq_status norm_rope(const rq_rope_config* cfg, int dtype, int weight_dtype, int 
     heads += x->x.heads;
     weights = weights || (back && x->weight_grad);
   }
+  if (back && q && k && q->weight_grad && k->weight_grad) {   // two sums in one place
+    const uintptr_t x = reinterpret_cast<uintptr_t>(q->weight_grad), y = reinterpret_cast<uintptr_t>(k->weight_grad);
+    if ((x < y ? y - x : x - y) < cfg->head_dim * sizeof(float)) return RQ_ERR_INVALID_ARG;
+  }
   if (heads * (batch > 0 ? batch : 1) > (1 << 30) || (int64_t)batch * n > (1 << 30)) return RQ_ERR_UNSUPPORTED;
   for (const rq_norm_tensor* x : {q, k})
     if (x && !empty && results_overlap({batch, x->x.heads, n}, {x->x.out_row, x->x.out_head, x->x.out_token}, cfg->head_dim))

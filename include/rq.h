@@ -628,7 +628,8 @@ rq_status rq_verify(int32_t rule, int32_t dtype, int32_t batch, int32_t n_nodes,
  *   weight       device [head_dim] of weight_dtype, shared by the heads; NULL: ones
  *   grad, grad_* backward: gradient of y, [batch][heads][n][d] of the tensor's type, its
  *                element strides; any strides, 0 included
- *   weight_grad  backward: device float32 [head_dim], receives the weight's gradient; NULL: not wanted */
+ *   weight_grad  backward: device float32 [head_dim], receives the weight's gradient; NULL: not wanted.  q's and k's
+ *                must not overlap: a weight that both share has the sum of the two */
 typedef struct rq_norm_tensor {
   rq_rope_tensor x;
   const void* weight;
@@ -658,7 +659,7 @@ size_t rq_norm_rope_workspace_bytes(int32_t head_dim);
  * weight_grad the weight's, summed over rows, heads and tokens in float32 in a fixed order (repeated calls
  * give equal bits).  No rows (batch or n 0): weight_grad is zero.  The workspace is needed where a weight_grad is
  * given, else it may be NULL; calls that may run at the same time need one each.
- * Errors: as rq_norm_rope; WORKSPACE. */
+ * Errors: as rq_norm_rope; INVALID_ARG (weight gradients that overlap); WORKSPACE. */
 rq_status rq_norm_rope_backward(const rq_rope_config* cfg, int32_t dtype, int32_t weight_dtype, int32_t batch,
                                 int32_t n, const rq_norm_tensor* q, const rq_norm_tensor* k, double eps,
                                 const int32_t* start, const int32_t* offsets, void* workspace,

@@ -56,3 +56,11 @@ def test_nothing_to_do(rq):
     assert call(rq, t(grad=None, weight_grad=None), n=0, back=True, ws=None) == OK
     assert rq.rq_norm_rope_workspace_bytes(1) == 0 and rq.rq_norm_rope_workspace_bytes(513) == 0
     assert rq.rq_norm_rope_workspace_bytes(512) > 0
+
+
+def test_weight_gradients_in_one_place(rq):
+    """The workspace is too small: what gets that far passed the check."""
+    t = lambda at: norm_tensor(rq, weight_grad=at)
+    go = lambda a, b: call(rq, t(a), t(b), back=True, size=0)
+    assert go(5 * P, 5 * P) == INVALID and go(5 * P, 5 * P + 508) == INVALID and go(5 * P + 4, 5 * P) == INVALID
+    assert go(5 * P, 5 * P + 512) == WORKSPACE and go(5 * P + 512, 5 * P) == WORKSPACE and go(5 * P, None) == WORKSPACE
