@@ -50,7 +50,7 @@ struct PlanLayout {
   int r_image, rt_image;                  // R and R^T as tensor-core operands, two BF16 pieces
   size_t words;
 };
-enum PlanHead { H_MAGIC, H_BATCH, H_N, H_NB, H_HEADS, H_QPK, H_TILES, H_ROT, H_WORDS = 8 };
+enum PlanHead { H_MAGIC, H_BATCH, H_N, H_NB, H_HEADS, H_QPK, H_TILES, H_ROT, H_TABLE, H_R = 10, H_WORDS = 12 };
 
 int plan_nb(const Geom& g, int batch, int n) {   // the average family's queries a KV head (see tree_nb's figures)
   const int64_t m = ((int64_t)batch * g.qpk + n - 1) / n;
@@ -65,6 +65,12 @@ bool own_tree(const Geom& g) { return g.qpk >= 3 && g.qpk <= kOwnNB; }
 
 // width and kind of the rotation
 __host__ __device__ constexpr int plan_rotation(const Geom& g) { return g.d << 8 | (g.mode & RQ_MODE_HADAMARD); }
+
+// where the plan's tables and rotation came from: two words each
+__device__ __forceinline__ int4 plan_origin(const Geom& g, const float* R) {
+  const uint64_t t = reinterpret_cast<uint64_t>(g.table), r = g.mode & RQ_MODE_HADAMARD ? 0 : reinterpret_cast<uint64_t>(R);
+  return make_int4((int)(uint32_t)t, (int)(t >> 32), (int)(uint32_t)r, (int)(r >> 32));
+}
 
 constexpr int image_words(int d) { return d * d; }   // two BF16 pieces of d x d
 
@@ -290,6 +296,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_families_kernel(PlanArgs a)
     a.plan[H_QPK] = a.g.qpk;
     a.plan[H_TILES] = l.ntiles;
     a.plan[H_ROT] = plan_rotation(a.g);
+    *reinterpret_cast<int4*>(a.plan + H_TABLE) = plan_origin(a.g, a.R);
     a.plan[H_MAGIC] = kPlanMagic;
   }
 }
@@ -345,6 +352,7 @@ struct PrefixArgs {
   Geom g;
   PlanLayout l;
   const int32_t* plan;
+  const float* R;
   const __nv_bfloat16 *q, *k_cur, *v_cur;
   const int32_t* seq_lens;
   __nv_bfloat16* out;
@@ -362,11 +370,12 @@ struct PrefixArgs {
   int o_ctas, qh;                  // qh: query heads of a decode unit
 };
 
-// Whether the plan is one of this shape (uniform over the grid).
+// Whether the plan is one of this shape, table and rotation (uniform over the grid).
 __device__ __forceinline__ bool plan_fits(const PrefixArgs& a) {
   const int4 x = __ldg(reinterpret_cast<const int4*>(a.plan)), y = __ldg(reinterpret_cast<const int4*>(a.plan) + 1);
+  const int4 z = __ldg(reinterpret_cast<const int4*>(a.plan) + 2), w = plan_origin(a.g, a.R);
   return x.x == kPlanMagic && x.y == a.l.batch && x.z == a.l.n && x.w == a.l.nb && y.x == a.g.H && y.y == a.g.qpk &&
-         y.z == a.l.ntiles && y.w == plan_rotation(a.g);
+         y.z == a.l.ntiles && y.w == plan_rotation(a.g) && z.x == w.x && z.y == w.y && z.z == w.z && z.w == w.w;
 }
 
 // 16 queries a CTA, neighbours in their family and of one KV head: as operands of the tensor-core kernel for the shared
@@ -1031,6 +1040,7 @@ cudaError_t launch_prefix(const rq_cache& c, int layer, int group, int loop, int
   a.g = g;
   a.l = l;
   a.plan = static_cast<const int32_t*>(plan);
+  a.R = c.R;
   a.q = q;
   a.k_cur = k_cur;
   a.v_cur = v_cur;

@@ -475,6 +475,7 @@ size_t rq_prefix_plan_bytes(const rq_config* cfg, int32_t batch, int32_t n_prefi
 
 /* Make the plan of rows 0 .. batch-1, from the block table, the lengths and the rows of each prompt.  It holds for
  * calls with these rows and lengths while the table and the rotation stay as they are: make it again once a row has grown.
+ * It belongs to the cache's block table and R (another cache of this shape over the same two may take it).
  *   n_prefixes     1 .. batch
  *   prefix_starts  device int32 [n_prefixes + 1]: prompt i's rows are prefix_starts[i] .. prefix_starts[i + 1] - 1 (any
  *                  number of them, none too).  Values are taken into 0 .. batch and never fall; the first counts as 0
@@ -489,7 +490,7 @@ rq_status rq_prefix_plan(rq_cache* cache, int32_t batch, int32_t n_prefixes, con
 
 /* Workspace (device bytes) of one rq_prefix_attention call on the current device (0 if invalid).  Zero-filled once
  * before its first use; the first 16 bytes are the status word, as under rq_decode_workspace_bytes, with [3] = 1
- * after a call whose plan was not one of its counts (out is not written then; [2] may be set, too) or of its lengths
+ * after a call whose plan was not one of its counts, table and R (out is not written then; [2] may be set, too) or of its lengths
  * (those of the plan are attended).  Calls that may run at the same time need a workspace each; they may share a plan. */
 size_t rq_prefix_workspace_bytes(const rq_config* cfg, int32_t batch, int32_t n_prefixes);
 
