@@ -334,3 +334,38 @@ def test_ends_of_the_range(dtype, d, r, top, eps):
         dx, dwr, bar, wbar = backward(rq, cfg, f64(z), f64(v), eps, pos, f64(y))
         close(got, dx, bar * 2.0 ** -18, dtype, "dx")
         close(gw, dwr, wbar * (2.0 ** -18 + 5 * nh * 2.0 ** -24), F, "dw")
+
+
+LONG = [
+    # as CASES: several items a CTA, across tokens, their number no multiple of the grid's
+    (BF, F, 128, 128, 0, 0, 0, 2, 5, 2, 4099, [0, 50000], False),
+    (HF, HF, 96, 64, 1, 0, 0, 2, 3, 2, 3001, [7, 1], True),
+    (F, F, 512, 256, 0, 0, 0, 2, 3, 1, 701, [9, 5], False),          # two slots a lane
+    (BF, F, 128, 58, 0, 0, 0, 2, 5, 2, 2501, [5, 900], False),       # the kernel for any alignment
+    (F, BF, 511, 254, 0, 0, 0, 2, 3, 1, 601, [3, 4], False),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=[f"{i}" for i in range(len(LONG))])
+def test_prompts(case):
+    """Forward into another tensor and in place, backward over the inputs: a CTA walks along heads and from token to token."""
+    rq, cfg, x, w, g, offs, pos = inputs(case, 11)
+    dtype, d, B, Hq, H, n = case[0], case[2], case[7], case[8], case[9], case[10]
+    start, offs = torch.tensor(case[11], dtype=torch.int32).cuda(), None if offs is None else offs.cuda()
+    dev, dg, wd = x.cuda(), g.cuda(), [v.cuda() for v in w]
+    q, k, qg, kg = heads(dev, 0, Hq), heads(dev, Hq, None), heads(dg, 0, Hq), heads(dg, Hq, None)
+    refs = [forward(rq, cfg, f64(z), f64(v), 1e-6, pos) for z, v in ((q, w[0]), (k, w[1]))]
+    back = [backward(rq, cfg, f64(z), f64(v), 1e-6, pos, f64(y)) for z, v, y in ((q, w[0], qg), (k, w[1], kg))]
+    out = torch.full_like(dev, 99)
+    rq.rq_norm_rope(cfg, q, k, *wd, 1e-6, start, offs, heads(out, 0, Hq), heads(out, Hq, None))
+    same = dev.clone()
+    rq.rq_norm_rope(cfg, heads(same, 0, Hq), heads(same, Hq, None), *wd, 1e-6, start, offs)
+    assert torch.equal(out, same)
+    for got, (ref, size) in zip((heads(out, 0, Hq), heads(out, Hq, None)), refs):
+        close(got, ref, size * 2.0 ** -18, dtype)
+    dw, ws = torch.full((2, d), 7.0, device="cuda"), torch.empty(rq.rq_norm_rope_workspace_bytes(d), dtype=torch.uint8,
+                                                                 device="cuda")
+    rq.rq_norm_rope_backward(cfg, q, k, qg, kg, *wd, 1e-6, start, offs, None, None, dw[0], dw[1], ws, ws.numel())
+    for got, gw, nh, (dx, dwr, bar, wbar) in ((q, dw[0], Hq, back[0]), (k, dw[1], H, back[1])):
+        close(got, dx, bar * 2.0 ** -18, dtype, "dx")
+        close(gw, dwr, wbar * (2.0 ** -18 + B * n * nh * 2.0 ** -24), F, "dw")
