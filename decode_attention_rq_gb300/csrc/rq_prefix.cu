@@ -16,10 +16,13 @@
 //   4. prefix_merge_kernel: both kinds of partial states, the current token, R^T, the quotient.
 //
 // Measured with 16 heads of 128, 32 rows of one 8192-token prompt and up to 512 tokens of their own (60 MB to read, 9 us at
-// the memory's rate), a residual loop: 43 us a call; every row alone 219.  Bound by latencies: the streaming kernel's 7 steps
-// a CTA with their start take 22 us, the rows' own tiles 10 to 14 more, the merge 6 behind them; the first steps of each
-// overlap the end of the one before.  64 rows of eight prompts, four query heads a KV head, groups of 16: 161 us against 41 at
-// the memory's rate, bound by dequantizing, as rq_tree_attention.
+// the memory's rate), a residual loop: 48 us a call; every row alone 219.  Bound by latencies: the streaming kernel's 7 steps
+// a CTA with their start take 22 us, the rows' own tiles 10 to 14 more, the merge 6 behind them, the prep 6 ahead; the first
+// steps of each overlap the end of the one before.  64 rows of eight prompts, four query heads a KV head, groups of 16: 161 us against 41 at
+// the memory's rate, bound by dequantizing, as rq_tree_attention (0.67 and 0.58 instructions a clock of each scheduler).
+// Two rows and one shared tile already make a family, whatever it costs: with 16 heads of 128 the call is faster than
+// rq_decode_attention from 4 rows of 8192 shared tokens (34 us for 37) or 32 rows of 512 (28 for 35) on, with four query
+// heads a KV head from 2 rows of 2048 (22 for 23) or 8 of 64 (20.6 for 21.2).  The plan takes 6.5 us, once a step.
 #include "rq_tree_kernels.cuh"
 #include "rq_decode_kernels.cuh"
 
@@ -59,8 +62,8 @@ int plan_nb(const Geom& g, int batch, int n) {   // the average family's queries
 
 // A row's own tiles go through the tensor-core kernel from three query heads a KV head on: a step of 128 tokens takes it the same
 // time for up to 16 of them.  Measured with 16 KV heads of 128, 32 rows of four 2048-token prompts, a call: four query heads
-// and tails of up to 1024 tokens 75 us (the decode kernel 86), up to 300 tokens in groups of 16 channels 55; two query
-// heads and up to 300 tokens 46 (the decode kernel 44).
+// and tails of up to 1024 tokens 72 us (the decode kernel 83), up to 300 tokens in groups of 16 channels 51 (71); three
+// query heads and up to 300 tokens 49 (65), two 44.8 (44.5).
 bool own_tree(const Geom& g) { return g.qpk >= 3 && g.qpk <= kOwnNB; }
 
 // width and kind of the rotation
@@ -83,7 +86,9 @@ PlanLayout plan_layout(const Geom& g, int batch, int n) {
   const int64_t queries = (int64_t)batch * g.qpk;
   const int64_t blocks = (queries + l.nb - 1) / l.nb + (n < batch / 2 ? n : batch / 2);   // a family that shares has two rows
   l.max_blocks = (int)(blocks < kPlanRows ? blocks : kPlanRows);
-  // queries a merge CTA: 8, or 16 where that still makes two CTAs an SM (R^T is then read half as often)
+  // queries a merge CTA: 8, or 16 where that still makes two CTAs on each of 152 SMs (R^T is then read half as often).  64
+  // query and 16 KV heads, 128 rows: 103 us with 16, 106 with 8 (512 CTAs); 55 heads of 96, 256 rows: 226 and 233; 80 rows
+  // in families of ten, whose last CTA of 16 is half empty: 83 and 79 (320); 64 rows: 62 and 64 (256)
   l.mq = g.H * ((queries + 15) / 16) >= 304 ? 16 : 8;
   l.max_merges = (int)((queries + l.mq - 1) / l.mq + n);
   l.max_preps = (int)((queries + kPrepQ - 1) / kPrepQ + n);

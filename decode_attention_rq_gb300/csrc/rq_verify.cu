@@ -42,7 +42,7 @@ constexpr int kMaxVocab = 262144;            // 8 slices of 32768: 129 KB of sha
 // Greedy: up to this many bytes of target rows all nodes' largest values are found at once, for reading them costs no more
 // than two or three nodes of a walk, some 3 us each (32 rows, 8 nodes, 50257 BF16 values: 9.3 us; walking 24).
 constexpr int64_t kAllNodesBytes = 32 << 20;
-constexpr int kFewCtas = 304;                // a node is split until two CTAs an SM are at work
+constexpr int kFewCtas = 304;                // a node is split until two CTAs are at work on each of 152 SMs
 
 struct VerifyArgs {
   const void *target, *draft;

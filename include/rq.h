@@ -466,7 +466,9 @@ rq_status rq_pages_compact(rq_cache* cache, int32_t* refs, int32_t* used, int32_
  * over such rows makes one plan (which tiles a prompt's rows share, how the work is split) and then calls
  * rq_prefix_attention for every layer, group and loop: the shared tiles are read once for all rows of
  * a prompt, on the tensor cores.  Results do not depend on what is shared, but for rounding: a row that shares nothing
- * is attended alone.  Paged caches of shared anchors (a cache of the contiguous layout: RQ_ERR_INVALID_ARG; chained:
+ * is attended alone.  It pays where rows and what they share are many: 16 heads of 128, against rq_decode_attention, from
+ * about 4 rows of 8192 shared tokens or 32 of 512 on; with four query heads per KV head from 2 rows of 2048 or 8 of
+ * 64.  Paged caches of shared anchors (a cache of the contiguous layout: RQ_ERR_INVALID_ARG; chained:
  * RQ_ERR_UNSUPPORTED).
  * --------------------------------------------------------------------------- */
 
